@@ -458,6 +458,171 @@ int kvq_step_destroy(kvq_step* step);
 /* Read the sticky status word into *out (host).  Synchronizes `stream`. */
 int kvq_get_status(const kvq_cache* cache, int32_t* out, void* stream);
 
+/*
+ * Paged 4-bit cache.  (No counterpart in the KVQuant pages: the serving form of this library's
+ * cache, for batches of requests of changing lengths.)  Keys and values are held in microscaled
+ * 4-bit floating point: a 4-bit code (E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) per
+ * channel, and one 8-bit scale (E4M3) per 16 channels, so a code converts in registers where the
+ * NUQ codes need a table.  4.5 bits per value.  Keys are stored as given (already rotated:
+ * kvq_rope).
+ *
+ * The pool is an array of pages; a page holds page_tokens tokens of every kv head:
+ *   pool uint8 [num_pages][Hkv][page_tokens/16][2][16*D/2 + 16*D/16]
+ * Inside (page, kv head, group of 16 tokens), keys (0) then values (1): 16 rows of D/2 code bytes
+ * (channel 2i in the low nibble of byte i, 2i + 1 in the high one), then 16 rows of D/16 scale
+ * bytes.  A token's slot is page * page_tokens + its row in the page; request b's token t lies in
+ * page block_table[b][t / page_tokens].  A value is code * scale * 2^k_exp (v_exp for values); the
+ * codes-times-scale product has 6 significant bits, so it is exact in fp16.
+ */
+#define KVQ_F16 0
+#define KVQ_BF16 1
+#define KVQ_F32 2 /* kvq_rope only */
+
+#define KVQ_STATUS_NO_PAGES 64  /* kvq_page_plan refused a request: the free list ran out */
+#define KVQ_STATUS_BAD_PAGE 128 /* a page number or slot outside the pool was skipped */
+
+typedef struct kvq_paged_cfg {
+    int32_t Hq;          /* query heads; a multiple of Hkv, at most 64 per kv head */
+    int32_t Hkv;         /* key/value heads, 1 .. 1024 */
+    int32_t D;           /* head dimension, 64 or 128 */
+    int32_t page_tokens; /* 16, 32, 64 or 128 */
+    int32_t num_pages;   /* pages of the pool; num_pages * page_tokens < 2^31 */
+    int32_t max_pages;   /* row width of the block tables: pages a request may have */
+    int32_t dtype;       /* KVQ_F16 or KVQ_BF16: keys, values, queries and outputs */
+    int32_t k_exp;       /* keys are stored divided by 2^k_exp, -64 .. 64: E4M3 scales reach from */
+    int32_t v_exp;       /* 2^-9 to 448, so a 16-channel maximum of 0.012 .. 2688 fits with 0 */
+} kvq_paged_cfg;
+
+typedef struct kvq_paged_cache {
+    uint8_t* pool;   /* kvq_paged_layout bytes; need not be cleared */
+    int32_t* status; /* int32 [1], sticky KVQ_STATUS_* bits */
+} kvq_paged_cache;
+
+/* Check a configuration: KVQ_OK, KVQ_ERR_NULL, KVQ_ERR_SHAPE, KVQ_ERR_RANGE, KVQ_ERR_UNSUPPORTED. */
+int kvq_paged_validate_cfg(const kvq_paged_cfg* cfg);
+
+/* Bytes of the pool. */
+int kvq_paged_layout(const kvq_paged_cfg* cfg, size_t* pool_bytes);
+
+/* Clear the status word (async on stream).  The pool needs no clearing. */
+int kvq_paged_reset(const kvq_paged_cache* cache, void* stream);
+
+/* Read the sticky status word into *out (host).  Synchronizes `stream`. */
+int kvq_paged_get_status(const kvq_paged_cache* cache, int32_t* out, void* stream);
+
+/*
+ * Block tables and slot maps of one scheduler step, from the requests' lengths.  Request b holds
+ * len[b] tokens in pages block_table[b][0 .. ceil(len[b]/P)) and brings n_new[b] more (P =
+ * page_tokens).  In request order, each takes the pages it lacks from the top of the free list
+ * (free_pages[n_free-1] first); a request that would pass max_pages pages, that finds too few
+ * free pages, or whose new tokens end past `capacity`, is refused: it keeps its length, its
+ * tokens get slot -1, and KVQ_STATUS_NO_PAGES (too few pages) or KVQ_STATUS_LEN_OVERFLOW is set.
+ * Once the list has run out no later request gets a page; one that needs none is still accepted.
+ *   len, n_new   int32 [B] (negative counts as 0);  block_table int32 [B][max_pages], updated
+ *   free_pages   int32 [num_pages], read;  n_free int32 [1], entries in use
+ *   capacity     host: entries of slots and positions
+ * Outputs (device):
+ *   cu_new int32 [B+1]  exclusive prefix sum of n_new: request b's tokens are
+ *                       [cu_new[b], cu_new[b+1]) of the step's packed token list
+ *   len_out int32 [B], n_free_out int32 [1]  after the step; each may be the input buffer itself
+ *   slots int32 [capacity]      cache slot of each packed token, -1 past cu_new[B]
+ *   positions int32 [capacity]  its position in its request, 0 past cu_new[B]
+ * The sum of n_new must be below 2^31.  One launch; nothing else is read back or cleared.
+ */
+int kvq_page_plan(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_t B,
+                  const int32_t* len, const int32_t* n_new, int32_t* block_table,
+                  const int32_t* free_pages, const int32_t* n_free, int32_t capacity,
+                  int32_t* cu_new, int32_t* len_out, int32_t* n_free_out, int32_t* slots,
+                  int32_t* positions, void* stream);
+
+/*
+ * Give back the pages of finished requests: for each b with done[b] != 0, in request order, its
+ * ceil(len[b]/P) pages go on top of the free list in table order, their table entries become -1
+ * and len[b] becomes 0.  n_free is updated in place.  Pages that would pass num_pages entries are
+ * dropped and set KVQ_STATUS_BAD_PAGE.
+ */
+int kvq_page_release(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_t B,
+                     int32_t* len, const int32_t* done, int32_t* block_table, int32_t* free_pages,
+                     int32_t* n_free, void* stream);
+
+/*
+ * Quantize n tokens into the pool: token i goes to slots[i] (a slot of -1 is skipped; one outside
+ * the pool too, with KVQ_STATUS_BAD_PAGE).  Per 16 channels x of a head, with y = x / 2^k_exp:
+ *   s = E4M3(max|y| / 6) (nearest even, at most 448), code = E2M1(y / s) (nearest even, at most
+ *   6 in size; 0 where s = 0).  A NaN is stored as 0 and left out of the maximum; an infinity is
+ *   stored as the largest value of its group.
+ *   k, v  16-bit [n][Hkv][D], rows k_stride and v_stride elements apart (a multiple of 8, at
+ *         least Hkv*D), 16-byte aligned.  slots int32 [n], distinct where not negative (where one
+ *         occurs twice, that slot's content is unspecified).
+ */
+int kvq_paged_append(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, const void* k,
+                     int64_t k_stride, const void* v, int64_t v_stride, const int32_t* slots,
+                     int32_t n, void* stream);
+
+/*
+ * Read n tokens back: khat, vhat 16-bit [n][Hkv][D] get code * scale * 2^exp of slots[i], rounded
+ * to the type (sizes past its largest finite value become that value); zeros for a slot of -1 or
+ * outside the pool (KVQ_STATUS_BAD_PAGE for the latter).
+ */
+int kvq_paged_dequantize(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache,
+                         const int32_t* slots, int32_t n, void* khat, void* vhat, void* stream);
+
+/*
+ * Attention of a ragged batch of queries over the paged cache: one token per request (decode), a
+ * few (drafts to verify) or a chunk of a prompt.  Request b's queries are the LAST
+ * n_b = cu_q[b+1] - cu_q[b] of its len[b] cached tokens: query i stands at position
+ * p = len[b] - n_b + i and sees the tokens t <= p, with window > 0 only those t > p - window.
+ *   x_t = sm_scale * q . khat_t,  out = sum_t e^(x_t - lse) vhat_t,  lse = log sum_t e^(x_t)
+ * over the seen tokens; a query that sees none (p < 0) gets out = 0, lse = -inf.  Pages numbered
+ * outside the pool count as not seen and set KVQ_STATUS_BAD_PAGE.
+ *   q     16-bit [total_q][Hq][D], rows q_stride elements apart (a multiple of 8, at least Hq*D),
+ *         16-byte aligned;  out 16-bit [total_q][Hq][D];  lse float [total_q][Hq] or NULL
+ *   cu_q  int32 [B+1], or NULL for one query per request (total_q = B); rows of q, out and lse
+ *         outside [cu_q[0], cu_q[B]) are not touched
+ *   max_q, max_len  host upper bounds on n_b and len[b]; queries and tokens past them are left
+ *         out and set KVQ_STATUS_LEN_OVERFLOW
+ *   splits  parts the token axis is cut into, 1 .. 256, or 0 for the library's choice
+ *   workspace  kvq_paged_attention_workspace bytes, 16-byte aligned (may be NULL when that is 0);
+ *         calls that may run at the same time need workspaces of their own
+ * The sums are taken in a fixed order: the same call returns the same bits.
+ */
+int kvq_paged_attention(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, const void* q,
+                        int64_t q_stride, const int32_t* cu_q, int32_t B, int32_t total_q,
+                        const int32_t* len, const int32_t* block_table, int32_t max_q,
+                        int32_t max_len, float sm_scale, int32_t window, void* out, float* lse,
+                        void* workspace, size_t workspace_bytes, int32_t splits, void* stream);
+
+/* Workspace bytes of kvq_paged_attention for the same sizes. */
+int kvq_paged_attention_workspace(const kvq_paged_cfg* cfg, int32_t B, int32_t total_q,
+                                  int32_t max_q, int32_t max_len, int32_t splits, size_t* bytes);
+
+/*
+ * Rotary positions with one or several axes (time, height, width), out of place or in place:
+ * pair i of the rot_dim/2 rotated pairs of every head turns by the angle
+ *   a = positions[pair_axis[i]][token] * freqs[i]   (binary64; cos and sin rounded to binary32)
+ *   (u, v) -> (u cos a - v sin a, v cos a + u sin a)
+ * with (u, v) = channels (i, i + rot_dim/2), or (2i, 2i + 1) when adjacent = 1.  Channels from
+ * rot_dim on are copied.  inverse = 1 turns by -a: the inverse map, and the gradient's.
+ *   q, k   [n][Hq][D], [n][Hkv][D] of cfg->dtype, token strides in elements (multiples of 16
+ *          bytes, at least H*D), 16-byte aligned; k may be NULL (then Hkv is 0).  An output is
+ *          either its input (same stride) or does not overlap any input.
+ *   positions int32 [axes][n];  freqs double [rot_dim/2] (device)
+ */
+typedef struct kvq_rope_cfg {
+    int32_t Hq, Hkv;    /* Hq >= 1, Hkv >= 0 */
+    int32_t D;          /* a multiple of 16, 16 .. 256 */
+    int32_t rot_dim;    /* a multiple of 16, 16 .. D */
+    int32_t dtype;      /* KVQ_F16, KVQ_BF16 or KVQ_F32 */
+    int32_t adjacent;   /* 0 or 1 */
+    int32_t axes;       /* 1 .. 8 */
+    uint8_t pair_axis[128]; /* axis of each pair, < axes */
+} kvq_rope_cfg;
+
+int kvq_rope(const kvq_rope_cfg* cfg, const void* q, int64_t q_stride, const void* k,
+             int64_t k_stride, const int32_t* positions, const double* freqs, int32_t n,
+             int32_t inverse, void* q_out, int64_t q_out_stride, void* k_out,
+             int64_t k_out_stride, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -9,7 +9,8 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_double, c_int, c_int32, c_size_t, c_void_p
+from ctypes import (POINTER, byref, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint8,
+                    c_void_p)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvq.so")
@@ -19,6 +20,8 @@ KVQ_STATUS_OUTLIER_OVERFLOW = 1
 KVQ_STATUS_LEN_OVERFLOW = 2
 KVQ_STATUS_NOT_EMPTY = 4
 KVQ_STATUS_WAIT_TIMEOUT = 8
+KVQ_STATUS_NO_PAGES = 64
+KVQ_STATUS_BAD_PAGE = 128
 CHUNK = 64
 NOALLOC_SCRATCH_BYTES = 1 << 20  # KVQ_NOALLOC_SCRATCH_BYTES
 
@@ -32,6 +35,9 @@ EXPORTS = (
     "kvq_decode_attention_fused", "kvq_decode_fused_workspace",
     "kvq_step_input_bytes", "kvq_step_workspace", "kvq_step_create", "kvq_step_launch",
     "kvq_step_destroy",
+    "kvq_paged_validate_cfg", "kvq_paged_layout", "kvq_paged_reset", "kvq_paged_get_status",
+    "kvq_page_plan", "kvq_page_release", "kvq_paged_append", "kvq_paged_dequantize",
+    "kvq_paged_attention", "kvq_paged_attention_workspace", "kvq_rope",
 )
 
 
@@ -70,6 +76,20 @@ class StepDesc(ctypes.Structure):
                 ("n_new", c_int32), ("max_len", c_int32), ("splits", c_int32), ("fused", c_int32),
                 ("inputs", c_void_p), ("out", c_void_p), ("workspace", c_void_p),
                 ("workspace_bytes", c_size_t)]
+
+
+class PagedCfg(ctypes.Structure):
+    _fields_ = [(f, c_int32) for f in ("Hq", "Hkv", "D", "page_tokens", "num_pages", "max_pages",
+                                       "dtype", "k_exp", "v_exp")]
+
+
+class PagedStruct(ctypes.Structure):
+    _fields_ = [("pool", c_void_p), ("status", c_void_p)]
+
+
+class RopeCfg(ctypes.Structure):
+    _fields_ = [(f, c_int32) for f in ("Hq", "Hkv", "D", "rot_dim", "dtype", "adjacent", "axes")]
+    _fields_ += [("pair_axis", c_uint8 * 128)]
 
 
 _lib = None
@@ -132,6 +152,20 @@ def load():
         "kvq_step_create": ([POINTER(Cfg), POINTER(StepDesc), POINTER(c_void_p)], c_int),
         "kvq_step_launch": ([P, P, P], c_int),
         "kvq_step_destroy": ([P], c_int),
+        "kvq_paged_validate_cfg": ([P], c_int),
+        "kvq_paged_layout": ([P, POINTER(c_size_t)], c_int),
+        "kvq_paged_reset": ([P, P], c_int),
+        "kvq_paged_get_status": ([P, POINTER(c_int32), P], c_int),
+        "kvq_page_plan": ([P, P, c_int32, P, P, P, P, P, c_int32, P, P, P, P, P, P], c_int),
+        "kvq_page_release": ([P, P, c_int32, P, P, P, P, P, P], c_int),
+        "kvq_paged_append": ([P, P, P, c_int64, P, c_int64, P, c_int32, P], c_int),
+        "kvq_paged_dequantize": ([P, P, P, c_int32, P, P, P], c_int),
+        "kvq_paged_attention": ([P, P, P, c_int64, P, c_int32, c_int32, P, P, c_int32, c_int32,
+                                 c_float, c_int32, P, P, P, c_size_t, c_int32, P], c_int),
+        "kvq_paged_attention_workspace": ([P, c_int32, c_int32, c_int32, c_int32, c_int32,
+                                           POINTER(c_size_t)], c_int),
+        "kvq_rope": ([P, P, c_int64, P, c_int64, P, P, c_int32, c_int32, P, c_int64, P, c_int64,
+                      P], c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -420,3 +454,233 @@ def kvq_get_status(cache: Cache, stream=None) -> int:
     _check(load().kvq_get_status(ctypes.byref(cache.struct), ctypes.byref(out), _stream(stream)),
            "kvq_get_status")
     return out.value
+
+
+# ------------------------------------------------------------------------- paged 4-bit cache
+# These calls check what a pointer cannot say -- types, shapes, strides, devices -- and raise
+# ValueError; they launch on the tensors' device, on `stream` or that device's current stream.
+
+def _dtype_code(dtype) -> int:
+    import torch
+    code = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}.get(dtype)
+    if code is None:
+        raise ValueError(f"dtype {dtype} is not float16, bfloat16 or float32")
+    return code
+
+
+def make_paged_cfg(Hq, Hkv, D, page_tokens, num_pages, max_pages, dtype, k_exp=0,
+                   v_exp=0) -> PagedCfg:
+    """dtype: torch.float16 or torch.bfloat16.  Raises KvqError where the library refuses it."""
+    cfg = PagedCfg(Hq, Hkv, D, page_tokens, num_pages, max_pages, _dtype_code(dtype), k_exp, v_exp)
+    _check(load().kvq_paged_validate_cfg(byref(cfg)), "kvq_paged_validate_cfg")
+    return cfg
+
+
+def kvq_paged_validate_cfg(cfg: PagedCfg) -> int:
+    return load().kvq_paged_validate_cfg(byref(cfg))
+
+
+def kvq_paged_layout(cfg: PagedCfg) -> int:
+    """Bytes of the pool."""
+    n = c_size_t()
+    _check(load().kvq_paged_layout(byref(cfg), byref(n)), "kvq_paged_layout")
+    return n.value
+
+
+class PagedCache:
+    """The pool of a paged 4-bit cache and its status word (one layer; the block tables, free list
+    and lengths belong to the requests and are shared by all layers)."""
+
+    def __init__(self, cfg: PagedCfg, device="cuda", pool=None):
+        import torch
+        self.cfg = cfg
+        n = kvq_paged_layout(cfg)
+        if pool is None:
+            pool = torch.empty(n, dtype=torch.uint8, device=device)
+        elif pool.dtype != torch.uint8 or pool.numel() < n or not pool.is_contiguous():
+            raise ValueError(f"PagedCache: the pool is a contiguous uint8 tensor of {n} bytes")
+        self.pool = pool
+        self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
+        self.device = pool.device
+        self.dtype = torch.bfloat16 if cfg.dtype else torch.float16
+        self.struct = PagedStruct(pool.data_ptr(), self.status.data_ptr())
+        self.args = byref(cfg), byref(self.struct)
+
+    def nbytes(self) -> int:
+        return self.pool.numel()
+
+
+def _call(where, fn, device, stream, *args):
+    """fn(*args, stream) on `device`, by its number."""
+    import torch
+    i = device.index
+    if device.type != "cuda":
+        raise ValueError(f"{where}: the tensors are on {device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(i)
+    if torch.cuda.current_device() == i:
+        code = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(i):
+            code = fn(*args, stream.cuda_stream)
+    if code != KVQ_OK:
+        raise KvqError(code, where)
+
+
+def _ints(where, device, **tensors):
+    import torch
+    for name, t in tensors.items():
+        if t.dtype != torch.int32 or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{where}: {name} is a contiguous int32 tensor on {device}")
+
+
+def _rows(where, name, t, shape, dtype, device):
+    """A [n, heads, D] tensor whose rows may lie apart; its row stride."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
+        raise ValueError(f"{where}: {name} is {tuple(t.shape)} {t.dtype} on {t.device}, not "
+                         f"{shape} {dtype} on {device}")
+    st = t.stride()
+    if (shape[2] > 1 and st[2] != 1) or (shape[1] > 1 and st[1] != shape[2]):
+        raise ValueError(f"{where}: {name}'s heads and channels are not contiguous")
+    return st[0] if shape[0] > 1 else shape[1] * shape[2]
+
+
+def kvq_paged_reset(cache: PagedCache, stream=None) -> None:
+    _call("kvq_paged_reset", load().kvq_paged_reset, cache.device, stream, cache.args[1])
+
+
+def kvq_paged_get_status(cache: PagedCache, stream=None) -> int:
+    out = c_int32()
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream(cache.device)
+    _check(load().kvq_paged_get_status(cache.args[1], byref(out), s.cuda_stream),
+           "kvq_paged_get_status")
+    return out.value
+
+
+def _table(where, cache, table, B):
+    _ints(where, cache.device, block_table=table)
+    if tuple(table.shape) != (B, cache.cfg.max_pages):
+        raise ValueError(f"{where}: block_table is {tuple(table.shape)}, not "
+                         f"{(B, cache.cfg.max_pages)}")
+
+
+def kvq_page_plan(cache: PagedCache, lens, n_new, block_table, free_pages, n_free, cu_new, len_out,
+                  n_free_out, slots, positions, stream=None) -> None:
+    w, B = "kvq_page_plan", lens.numel()
+    _ints(w, cache.device, lens=lens, n_new=n_new, free_pages=free_pages, n_free=n_free,
+          cu_new=cu_new, len_out=len_out, n_free_out=n_free_out, slots=slots, positions=positions)
+    _table(w, cache, block_table, B)
+    cap = slots.numel()
+    if (n_new.numel() != B or cu_new.numel() != B + 1 or len_out.numel() != B
+            or n_free.numel() != 1 or n_free_out.numel() != 1 or positions.numel() != cap):
+        raise ValueError(f"{w}: sizes do not agree with {B} requests and {cap} tokens")
+    _call(w, load().kvq_page_plan, cache.device, stream, *cache.args, B, lens.data_ptr(),
+          n_new.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(), cap,
+          cu_new.data_ptr(), len_out.data_ptr(), n_free_out.data_ptr(), slots.data_ptr(),
+          positions.data_ptr())
+
+
+def kvq_page_release(cache: PagedCache, lens, done, block_table, free_pages, n_free,
+                     stream=None) -> None:
+    w, B = "kvq_page_release", lens.numel()
+    _ints(w, cache.device, lens=lens, done=done, free_pages=free_pages, n_free=n_free)
+    _table(w, cache, block_table, B)
+    if done.numel() != B or n_free.numel() != 1 or free_pages.numel() < cache.cfg.num_pages:
+        raise ValueError(f"{w}: sizes do not agree with {B} requests and {cache.cfg.num_pages} pages")
+    _call(w, load().kvq_page_release, cache.device, stream, *cache.args, B, lens.data_ptr(),
+          done.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), n_free.data_ptr())
+
+
+def kvq_paged_append(cache: PagedCache, k, v, slots, stream=None) -> None:
+    w, c, n = "kvq_paged_append", cache.cfg, slots.numel()
+    _ints(w, cache.device, slots=slots)
+    ks = _rows(w, "k", k, (n, c.Hkv, c.D), cache.dtype, cache.device)
+    vs = _rows(w, "v", v, (n, c.Hkv, c.D), cache.dtype, cache.device)
+    _call(w, load().kvq_paged_append, cache.device, stream, *cache.args, k.data_ptr(), ks,
+          v.data_ptr(), vs, slots.data_ptr(), n)
+
+
+def kvq_paged_dequantize(cache: PagedCache, slots, khat, vhat, stream=None) -> None:
+    w, c, n = "kvq_paged_dequantize", cache.cfg, slots.numel()
+    _ints(w, cache.device, slots=slots)
+    for name, t in (("khat", khat), ("vhat", vhat)):
+        if _rows(w, name, t, (n, c.Hkv, c.D), cache.dtype, cache.device) != c.Hkv * c.D:
+            raise ValueError(f"{w}: {name} is not contiguous")
+    _call(w, load().kvq_paged_dequantize, cache.device, stream, *cache.args, slots.data_ptr(), n,
+          khat.data_ptr(), vhat.data_ptr())
+
+
+def kvq_paged_attention_workspace(cfg: PagedCfg, B: int, total_q: int, max_q: int, max_len: int,
+                                  splits: int = 0) -> int:
+    n = c_size_t()
+    _check(load().kvq_paged_attention_workspace(byref(cfg), B, total_q, max_q, max_len, splits,
+                                                byref(n)), "kvq_paged_attention_workspace")
+    return n.value
+
+
+def kvq_paged_attention(cache: PagedCache, q, cu_q, lens, block_table, max_q: int, max_len: int,
+                        sm_scale: float, out, workspace=None, window: int = 0, lse=None,
+                        splits: int = 0, stream=None) -> None:
+    """cu_q: int32 [B + 1], or None for one query per request."""
+    w, c, dev, B, n = "kvq_paged_attention", cache.cfg, cache.device, lens.numel(), q.shape[0]
+    _ints(w, dev, lens=lens)
+    _table(w, cache, block_table, B)
+    qs = _rows(w, "q", q, (n, c.Hq, c.D), cache.dtype, dev)
+    if _rows(w, "out", out, (n, c.Hq, c.D), cache.dtype, dev) != c.Hq * c.D:
+        raise ValueError(f"{w}: out is not contiguous")
+    cu = l = ws = None
+    wb = 0
+    if cu_q is not None:
+        _ints(w, dev, cu_q=cu_q)
+        if cu_q.numel() != B + 1:
+            raise ValueError(f"{w}: cu_q has {cu_q.numel()} entries for {B} requests")
+        cu = cu_q.data_ptr()
+    if lse is not None:
+        import torch
+        if (lse.dtype != torch.float32 or lse.device != dev or tuple(lse.shape) != (n, c.Hq)
+                or not lse.is_contiguous()):
+            raise ValueError(f"{w}: lse is a contiguous float32 tensor {(n, c.Hq)} on {dev}")
+        l = lse.data_ptr()
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"{w}: the workspace is a contiguous tensor on {dev}")
+        ws, wb = workspace.data_ptr(), workspace.nbytes
+    _call(w, load().kvq_paged_attention, dev, stream, *cache.args, q.data_ptr(), qs, cu, B, n,
+          lens.data_ptr(), block_table.data_ptr(), max_q, max_len, sm_scale, window,
+          out.data_ptr(), l, ws, wb, splits)
+
+
+def make_rope_cfg(Hq, Hkv, D, rot_dim, pair_axis, dtype, adjacent=False) -> RopeCfg:
+    """pair_axis: the axis (0, 1, ...) of each of the rot_dim/2 pairs, as a list."""
+    axes = [int(x) for x in pair_axis]
+    if len(axes) != rot_dim // 2 or len(axes) > 128 or min(axes, default=-1) < 0 or max(axes) > 7:
+        raise ValueError(f"make_rope_cfg: pair_axis names an axis (0 .. 7) for each of the "
+                         f"{rot_dim // 2} pairs")
+    return RopeCfg(Hq, Hkv, D, rot_dim, _dtype_code(dtype), int(bool(adjacent)), max(axes) + 1,
+                   (c_uint8 * 128)(*axes))
+
+
+def kvq_rope(cfg: RopeCfg, q, k, positions, freqs, q_out, k_out, inverse=False,
+             stream=None) -> None:
+    """q, k [n, heads, D] (k may be None when cfg.Hkv is 0), positions int32 [axes, n], freqs
+    float64 [rot_dim / 2]; q_out and k_out may be q and k."""
+    import torch
+    w, n, dev = "kvq_rope", q.shape[0], q.device
+    dtype = (torch.float16, torch.bfloat16, torch.float32)[cfg.dtype]
+    _ints(w, dev, positions=positions)
+    if tuple(positions.shape) != (cfg.axes, n) and not (cfg.axes == 1 and positions.numel() == n):
+        raise ValueError(f"{w}: positions is {tuple(positions.shape)}, not {(cfg.axes, n)}")
+    if (freqs.dtype != torch.float64 or freqs.numel() != cfg.rot_dim // 2 or freqs.device != dev
+            or not freqs.is_contiguous()):
+        raise ValueError(f"{w}: freqs is a float64 tensor of {cfg.rot_dim // 2} on {dev}")
+    qs = _rows(w, "q", q, (n, cfg.Hq, cfg.D), dtype, dev)
+    qos = _rows(w, "q_out", q_out, (n, cfg.Hq, cfg.D), dtype, dev)
+    kp = kop = None
+    ks = kos = 0
+    if cfg.Hkv:
+        ks = _rows(w, "k", k, (n, cfg.Hkv, cfg.D), dtype, dev)
+        kos = _rows(w, "k_out", k_out, (n, cfg.Hkv, cfg.D), dtype, dev)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    _call(w, load().kvq_rope, dev, stream, byref(cfg), q.data_ptr(), qs, kp, ks,
+          positions.data_ptr(), freqs.data_ptr(), n, int(inverse), q_out.data_ptr(), qos, kop, kos)
