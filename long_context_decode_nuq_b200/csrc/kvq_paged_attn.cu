@@ -1,5 +1,5 @@
 // Attention over the paged 4-bit cache: one token, a few or a chunk of them per request.
-#include "kvq_paged.cuh"
+#include "kvq_paged_attn.cuh"
 
 using namespace kvq;
 using namespace kvq_host;
@@ -26,37 +26,6 @@ namespace {
 // reads of V rows spread over the banks; S^T then leaves its lanes with (token, 2 rows), which
 // movmatrix turns into the B operand of the second product.
 constexpr int kTile = 32;
-constexpr float kPShift = 12.0f;  // P is e^(x - m) 2^12 ...
-constexpr float kPRoom = 15.0f;   // ... and may grow to 2^15 before m is moved
-
-struct AttnArgs {
-    kvq_paged_cfg c;
-    const uint8_t* pool;
-    int32_t* status;
-    const uint16_t* q;
-    int64_t qs;
-    const int32_t *cu, *len, *table;
-    uint16_t* out;
-    float *lse, *part;
-    float2* pml;
-    int32_t total_q, max_q, max_len, window, S;
-    float scale_log2, out_scale;
-};
-
-// The rows and tokens of a (request, row block), the same in the main kernel and the merge.
-struct Rows {
-    int c0, n, nq, R, len, kv;
-};
-__device__ __forceinline__ Rows rows_of(const AttnArgs& a, int b) {
-    Rows r;
-    r.c0 = a.cu ? min(max(a.cu[b], 0), a.total_q) : b;
-    r.n = a.cu ? min(max(a.cu[b + 1] - a.cu[b], 0), a.total_q - r.c0) : 1;
-    r.nq = min(r.n, a.max_q);
-    r.R = r.nq * (a.c.Hq / a.c.Hkv);
-    r.len = max(a.len[b], 0);
-    r.kv = min(min(r.len, a.max_len), a.c.max_pages * a.c.page_tokens);
-    return r;
-}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -81,11 +50,6 @@ constexpr int attn_smem() {
     constexpr int ring = Shape<NT>::W * Shape<NT>::ST * 2 * Paged<D>::kBytes;
     constexpr int join = Shape<NT>::W * 8 * NT * (D + 4 + 2) * 4;
     return (ring > join ? ring : join) + 8 * Shape<NT>::W * Shape<NT>::ST;
-}
-
-template <bool BF>
-__device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack16<BF>(a, b), pack16<BF>(c, d));
 }
 
 template <int D, int NT, bool BF>
@@ -404,7 +368,7 @@ __global__ void __launch_bounds__(Shape<NT>::W * 32, NT == 1 ? 2 : 1)
         if (a.S == 1) {
             const float inv = L == 0.0f ? 0.0f : a.out_scale / L;
             store4<BF>(a.out + grow * D + c4, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-            if (c4 == 0 && a.lse) a.lse[grow] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+            if (c4 == 0 && a.lse) a.lse[grow] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
         } else {
             *reinterpret_cast<float4*>(a.part + (s * nrow + grow) * D + c4) = acc;
             if (c4 == 0) a.pml[s * nrow + grow] = make_float2(M, L);
@@ -442,35 +406,58 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const AttnArgs
 #pragma unroll
     for (int i = 0; i < D / 32; i += 2)
         *reinterpret_cast<uint32_t*>(out + i) = pack16<BF>(acc[i] * inv, acc[i + 1] * inv);
-    if (lane == 0 && a.lse) a.lse[grow] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+    if (lane == 0 && a.lse) a.lse[grow] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 // ---------------------------------------------------------------------------------
-// Host: rows per block, splits.
+// Host: which kernel, rows per block, splits.
 struct Plan {
-    int nt, nrb, S;
+    int nt;  // 8-row tiles of a block of k_paged_attn; 0: the chunk kernel
+    int nrb, S;
 };
+
+constexpr int kSms = 148;
+// More rows of a kv head than this go to the chunk kernel.
+constexpr int kFewRows = 32;
+
+// Splits of the chunk kernel: the least time of a model in which a block costs 6 us and 1.2 us per
+// 128 tokens, blocks run one per SM in waves, and a split writes and reads its part at 5 TB/s.
+int chunk_splits(const kvq_paged_cfg* c, int64_t units, int64_t tiles) {
+    int best = 1;
+    double least = 1e30;
+    for (int S = 1; S <= 32 && S <= tiles; ++S) {
+        const int64_t waves = (units * S + kSms - 1) / kSms;
+        double t = (double)waves * (6.0 + 1.2 * (double)((tiles + S - 1) / S));
+        if (S > 1) t += 4.0 + (double)units * S * kChunkRows * c->D * 8 / 5e6;
+        if (t < 0.98 * least) least = t, best = S;
+    }
+    return best;
+}
+
+int splits_of(const kvq_paged_cfg* c, const Plan& p, int B, int64_t span) {
+    const int64_t units = (int64_t)B * c->Hkv * p.nrb;
+    if (p.nt == 0) return chunk_splits(c, units, (span + 127) / 128);
+    // the tokens a row block can see bound the useful splits at a tile a warp
+    const int warps = p.nt == 1 ? 8 : 4;
+    const int64_t tiles = (span + kTile - 1) / kTile;
+    int64_t S = (kSms * 4 + units - 1) / units;
+    const int64_t most = (tiles + warps - 1) / warps;
+    if (S > most) S = most;
+    return (int)(S > 256 ? 256 : S < 1 ? 1 : S);
+}
 
 Plan plan_of(const kvq_paged_cfg* c, int B, int max_q, int max_len, int splits, int window) {
     const int64_t R = (int64_t)max_q * (c->Hq / c->Hkv);
     Plan p;
-    p.nt = R <= 8 ? 1 : R <= 16 ? 2 : 4;
-    p.nrb = (int)((R + 8 * p.nt - 1) / (8 * p.nt));
-    const int warps = p.nt == 1 ? 8 : 4;
-    // the tokens a row block can see bound the useful splits at a tile a warp
-    int64_t span = max_len;
-    if (window > 0 && span > (int64_t)window + max_q + kTile) span = (int64_t)window + max_q + kTile;
-    const int64_t tiles = (span + kTile - 1) / kTile;
-    int64_t S = splits;
-    if (S == 0) {
-        const int64_t units = (int64_t)B * c->Hkv * p.nrb;
-        S = (148 * 4 + units - 1) / units;
-        const int64_t most = (tiles + warps - 1) / warps;
-        if (S > most) S = most;
-        if (S > 256) S = 256;
-        if (S < 1) S = 1;
+    p.nt = R <= 8 ? 1 : R <= 16 ? 2 : R <= kFewRows ? 4 : 0;
+    const int rows = p.nt ? 8 * p.nt : kChunkRows;
+    p.nrb = (int)((R + rows - 1) / rows);
+    p.S = splits ? splits : splits_of(c, p, B, max_len);
+    if (!splits && window > 0 && max_len > (int64_t)window + max_q + 128) {
+        // a window only lowers the splits: the workspace is sized without it
+        const int S = splits_of(c, p, B, (int64_t)window + max_q + 128);
+        if (S < p.S) p.S = S;
     }
-    p.S = (int)S;
     return p;
 }
 
@@ -549,24 +536,29 @@ int kvq_paged_attention(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, 
     a.scale_log2 = (float)ldexp((double)sm_scale * 1.4426950408889634, cfg->k_exp);
     a.out_scale = ldexpf(1.0f, cfg->v_exp);
     const bool bf = cfg->dtype == KVQ_BF16;
+    cudaError_t ce;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (p.nt == 0) {
+        if ((e = run_chunk(a, p.nrb, B, st))) return e;
+    } else {
     int smem, warps;
     const AttnKernel kern = cfg->D == 64 ? (bf ? attn_kernel<64, true>(p.nt, &smem, &warps)
                                                : attn_kernel<64, false>(p.nt, &smem, &warps))
                                          : (bf ? attn_kernel<128, true>(p.nt, &smem, &warps)
                                                : attn_kernel<128, false>(p.nt, &smem, &warps));
-    cudaError_t ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (ce) return record_cuda(ce);
-    cudaStream_t st = (cudaStream_t)stream;
     kern<<<dim3((unsigned)(p.S * p.nrb), cfg->Hkv, B), warps * 32, smem, st>>>(a);
     if ((ce = cudaGetLastError())) return record_cuda(ce);
+    }
     if (p.S > 1) {
         auto* mk = cfg->D == 64 ? (bf ? k_paged_merge<64, true> : k_paged_merge<64, false>)
                                 : (bf ? k_paged_merge<128, true> : k_paged_merge<128, false>);
         const int64_t R = (int64_t)max_q * (cfg->Hq / cfg->Hkv);
         mk<<<dim3((unsigned)((R + kMergeWarps - 1) / kMergeWarps), cfg->Hkv, B), kMergeWarps * 32, 0, st>>>(a);
-        ce = cudaGetLastError();
+        return record_cuda(cudaGetLastError());
     }
-    return record_cuda(ce);
+    return KVQ_OK;
 }
 
 }  // extern "C"

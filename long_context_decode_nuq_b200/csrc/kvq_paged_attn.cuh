@@ -1,0 +1,52 @@
+// What the two attention kernels over the paged cache share.
+#pragma once
+
+#include "kvq_paged.cuh"
+
+namespace kvq {
+
+constexpr float kPShift = 12.0f;  // P is held as e^(x - max) 2^12 ...
+constexpr float kPRoom = 15.0f;   // ... and may grow to 2^15 before the maximum is moved
+constexpr float kLn2 = 0.69314718055994531f;
+
+struct AttnArgs {
+    kvq_paged_cfg c;
+    const uint8_t* pool;
+    int32_t* status;
+    const uint16_t* q;
+    int64_t qs;
+    const int32_t *cu, *len, *table;
+    uint16_t* out;
+    float *lse, *part;
+    float2* pml;
+    int32_t total_q, max_q, max_len, window, S;
+    float scale_log2, out_scale;
+};
+
+// The rows and tokens of a (request, row block), the same in the main kernel and the merge.
+struct Rows {
+    int c0, n, nq, R, len, kv;
+};
+__device__ __forceinline__ Rows rows_of(const AttnArgs& a, int b) {
+    Rows r;
+    r.c0 = a.cu ? min(max(a.cu[b], 0), a.total_q) : b;
+    r.n = a.cu ? min(max(a.cu[b + 1] - a.cu[b], 0), a.total_q - r.c0) : 1;
+    r.nq = min(r.n, a.max_q);
+    r.R = r.nq * (a.c.Hq / a.c.Hkv);
+    r.len = max(a.len[b], 0);
+    r.kv = min(min(r.len, a.max_len), a.c.max_pages * a.c.page_tokens);
+    return r;
+}
+
+template <bool BF>
+__device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack16<BF>(a, b), pack16<BF>(c, d));
+}
+
+}  // namespace kvq
+
+namespace kvq_host {
+// Prompt chunks (kvq_paged_chunk.cu): query rows of a block, and the launch.
+constexpr int kChunkRows = 256;
+int run_chunk(const kvq::AttnArgs& a, int nrb, int B, cudaStream_t stream);
+}  // namespace kvq_host
