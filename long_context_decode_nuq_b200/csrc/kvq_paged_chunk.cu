@@ -13,8 +13,8 @@ namespace {
 // from there.  Roles, by warp:
 //   0-3, 4-7   softmax of a row tile, a thread a row: scores out of tensor memory, maximum, e^x,
 //              P back; the maximum moves only when it has grown by 2^3, so O is seldom rescaled
-//   8-11       codes to fp16 in shared memory (a 128-byte swizzled tile of K or V, three slots)
-//   12         bulk copies of the codes, a lane a group of 16 tokens, two tiles ahead
+//   8-11       codes to fp16 in shared memory (a 128-byte swizzled tile of K or V, four slots)
+//   12         bulk copies of the codes, a lane a group of 16 tokens, three tiles ahead
 //   13         one thread issues the products:  S_i = Q_i K^T,  O_i += P_i V
 // The two row tiles alternate, so one's softmax runs under the other's products, and each
 // dequantized tile serves both: 32768 conversions feed 2 x 128 x 128 x D x 2 multiply-adds.
@@ -24,8 +24,8 @@ namespace {
 // tokens be issued behind the product that still reads P_i from the same columns.
 constexpr int kRows = kChunkRows;   // 2 tiles of 128
 constexpr int kTok = 128;           // tokens a step
-constexpr int kSlots = 3;           // K/V tiles in shared memory
-constexpr int kRaw = 2;             // code tiles in flight
+constexpr int kSlots = 4;           // K or V tiles in shared memory
+constexpr int kRaw = 3;             // code tiles (of K or V) in flight
 constexpr int kThreads = 512;
 constexpr uint32_t kPollLimit = 1u << 22;
 // registers per thread after the split; their sum over the four warpgroups stays within the
@@ -37,10 +37,10 @@ struct Smem {
     static constexpr int q = 0;                              // [D/64][256][128 B] swizzled
     static constexpr int slot = kRows * D * 2;               // [kSlots][D/64][128][128 B] swizzled
     static constexpr int slot_bytes = kTok * D * 2;
-    static constexpr int raw = slot + kSlots * slot_bytes;   // [kRaw][8 groups]
-    static constexpr int raw_bytes = kTok / kGroup * Paged<D>::kBytes;
+    static constexpr int raw = slot + kSlots * slot_bytes;   // [kRaw][8 groups]: keys or values
+    static constexpr int raw_bytes = kTok / kGroup * Paged<D>::kHalf;
     static constexpr int bar = raw + kRaw * raw_bytes;
-    static constexpr int n_bar = 2 * kRaw + 2 * kSlots + 6;
+    static constexpr int n_bar = 2 * kRaw + 2 * kSlots + 8;
     static constexpr int misc = bar + 8 * n_bar;             // tmem address, dead flag, group masks
     static constexpr int total = misc + 64;
 };
@@ -80,6 +80,11 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 template <int N>
@@ -89,6 +94,12 @@ __device__ __forceinline__ void regs_up() {
 template <int N>
 __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 // 32 or 64 columns of the warp's 32 lanes, from and to tensor memory.
@@ -145,8 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
     uint64_t* kv_full = raw_empty + kRaw;
     uint64_t* kv_empty = kv_full + kSlots;
     uint64_t* s_full = kv_empty + kSlots;  // [2]
-    uint64_t* p_full = s_full + 2;         // [2]
-    uint64_t* pv_done = p_full + 2;        // [2]
+    uint64_t* p_full = s_full + 2;         // [2][2]: P's first and second 64 columns
+    uint64_t* pv_done = p_full + 4;        // [2]
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + L::misc);
     volatile int* dead = reinterpret_cast<volatile int*>(smem + L::misc + 4);
     uint8_t* gmask = smem + L::misc + 8;   // [8] groups that were brought, of the last 8 tiles
@@ -180,7 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
         *dead = 0;
         for (int i = 0; i < kRaw; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 4);
         for (int i = 0; i < kSlots; ++i) mbar_init(&kv_full[i], 4), mbar_init(&kv_empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4), mbar_init(&pv_done[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&pv_done[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 4);
         fence_mbar_init();
     }
     // queries: a thread a row, its power of two kept for the scores
@@ -231,6 +243,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
             for (int j = 0; j < n; ++j) {
                 if (!__all_sync(0xffffffffu, wait_on(&s_full[i], j & 1, dead))) break;
                 fence_after();
+                // these scores are complete, and with them all that was issued before: K_j's slot
+                // and V_(j-1)'s are free
+                if (i == nact - 1 && (threadIdx.x & 127) == 0) {
+                    mbar_arrive(&kv_empty[2 * j % kSlots]);
+                    if (j > 0) mbar_arrive(&kv_empty[(2 * j - 1) % kSlots]);
+                }
                 uint32_t x[2][64];
                 tmem_ld64(x[0], st);
                 tmem_ld64(x[1], st + 64);
@@ -243,18 +261,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
                         if (!(t < hi_r && t >= lo_r && (got >> (c / kGroup) & 1u))) x[c / 64][c % 64] = 0xff800000u;
                     }
                 }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float mx[8];
 #pragma unroll
-                for (int c = 0; c < kTok; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c / 64][c % 64]));
-                const float tm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                for (int c = 0; c < 8; ++c) mx[c] = __uint_as_float(x[0][c]);
+#pragma unroll
+                for (int c = 8; c < kTok; c += 16)
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) {
+                        const float y = __uint_as_float(x[c / 64][c % 64 + z]);
+                        mx[z] = c + 8 < kTok ? fmaxf(mx[z], fmaxf(y, __uint_as_float(x[(c + 8) / 64 % 2][(c + 8) % 64 + z]))) : fmaxf(mx[z], y);
+                    }
+                const float tm = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sl2;
                 if (__any_sync(0xffffffffu, tm - m > kPRoom)) {
                     const float mn = fmaxf(m, tm - kPShift);
                     const float al = m == mn ? 1.0f : ex2(m - mn);
                     m = mn;
                     l *= al;
-                    if (j > 0) {  // O of the steps before must be complete, and is rescaled
-                        if (!__all_sync(0xffffffffu, wait_on(&pv_done[i], (j - 1) & 1, dead))) break;
-                        fence_after();
+                    if (j > 0) {  // O is complete up to the step before, as S of this one is
 #pragma unroll
                         for (int c = 0; c < D; c += 32) {
                             uint32_t o[32];
@@ -273,22 +296,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
                     uint32_t p[32];
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
-                        const f2 y = upk(fma2(pk(__uint_as_float(x[half][2 * c]), __uint_as_float(x[half][2 * c + 1])), sl2p, nmp));
-                        const float e0 = ex2(y.x), e1 = ex2(y.y);
-                        sum[c & 1] = fma2(pk(e0, e1), pk(1.0f, 1.0f), sum[c & 1]);
+                        const unsigned long long y = fma2(pk(__uint_as_float(x[half][2 * c]), __uint_as_float(x[half][2 * c + 1])), sl2p, nmp);
+                        const f2 z = upk(y);
+                        const float e0 = ex2(z.x), e1 = ex2(z.y);
+                        sum[c & 1] = add2(sum[c & 1], pk(e0, e1));
                         p[c] = pack_h2(e0, e1);
                     }
                     tmem_st32(st + half * 32, p);
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * i + half]);
                 }
                 const f2 u = upk(sum[0]), v = upk(sum[1]);
                 l += (u.x + u.y) + (v.x + v.y);
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[i]);
             }
         // the row's output
         if (i < nact && n > 0) {
-            __all_sync(0xffffffffu, wait_on(&pv_done[i], (n - 1) & 1, dead));
+            __all_sync(0xffffffffu, wait_on(&pv_done[i], 0, dead));
             fence_after();
         }
         const bool real = i < nact && r < rw.R;
@@ -332,50 +356,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
         constexpr int LPR = D / 32;          // lanes of a token's row, 16 code bytes each
         constexpr int RPP = 128 / LPR;       // rows a pass
         const int q = tid % LPR, rr = tid / LPR;
-        bool ok = true;
-        for (int j = 0; j < n && ok; ++j) {
-            const int rs = j % kRaw;
-            ok = __all_sync(0xffffffffu, wait_on(&raw_full[rs], (j / kRaw) & 1, dead));
-            if (!ok) break;
+        for (int seq = 0; seq < 2 * n; ++seq) {  // K_0, V_0, K_1, ...
+            const int rs = seq % kRaw, slot = seq % kSlots, j = seq >> 1;
+            const bool val = seq & 1;
+            if (!__all_sync(0xffffffffu, wait_on(&raw_full[rs], (seq / kRaw) & 1, dead) &&
+                                             wait_on(&kv_empty[slot], (seq / kSlots + 1) & 1, dead)))
+                break;
             const uint32_t got = gmask[j & 7];
             const int t0 = tok0 + j * kTok;
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {  // keys, then values
-                const int seq = 2 * j + half, slot = seq % kSlots;
-                ok = __all_sync(0xffffffffu, wait_on(&kv_empty[slot], (seq / kSlots + 1) & 1, dead));
-                if (!ok) break;
-                uint8_t* dst = smem + L::slot + slot * L::slot_bytes + (q >> 1) * (kTok * 128);
-                const uint8_t* src = smem + L::raw + rs * L::raw_bytes + half * Paged<D>::kHalf;
+            uint8_t* dst = smem + L::slot + slot * L::slot_bytes + (q >> 1) * (kTok * 128);
+            const uint8_t* src = smem + L::raw + rs * L::raw_bytes;
 #pragma unroll
-                for (int pass = 0; pass < LPR; ++pass) {
-                    const int t = pass * RPP + rr;
-                    const uint8_t* g = src + (t / kGroup) * Paged<D>::kBytes;
-                    const uint4 c4 = *reinterpret_cast<const uint4*>(g + (t % kGroup) * Paged<D>::kRow + q * 16);
-                    uint32_t sc = *reinterpret_cast<const uint16_t*>(g + kGroup * Paged<D>::kRow + (t % kGroup) * Paged<D>::kScales + q * 2);
-                    // bytes nobody wrote may hold NaN scales; as values they must be 0
-                    if (half && (t0 + t >= rw.kv || !(got >> (t / kGroup) & 1u))) sc = 0;
-                    const uint32_t two = e4m3x2(sc);
-                    const uint32_t s2[2] = {__byte_perm(two, 0, 0x1010), __byte_perm(two, 0, 0x3232)};
-                    const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
-                    // the lanes of the second half of the channels go in another order, so that
-                    // eight lanes write eight different 16-byte columns
-                    const int flip = D == 128 ? (q >> 1) * 2 : 0;
+            for (int pass = 0; pass < LPR; ++pass) {
+                const int t = pass * RPP + rr;
+                const uint8_t* g = src + (t / kGroup) * Paged<D>::kHalf;
+                const uint4 c4 = *reinterpret_cast<const uint4*>(g + (t % kGroup) * Paged<D>::kRow + q * 16);
+                uint32_t sc = *reinterpret_cast<const uint16_t*>(g + kGroup * Paged<D>::kRow + (t % kGroup) * Paged<D>::kScales + q * 2);
+                // bytes nobody wrote may hold NaN scales; as values they must be 0
+                if (val && (t0 + t >= rw.kv || !(got >> (t / kGroup) & 1u))) sc = 0;
+                const uint32_t two = e4m3x2(sc);
+                const uint32_t s2[2] = {__byte_perm(two, 0, 0x1010), __byte_perm(two, 0, 0x3232)};
+                const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
+                // the lanes of the second half of the channels go in another order, so that
+                // eight lanes write eight different 16-byte columns
+                const int flip = D == 128 ? (q >> 1) * 2 : 0;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t word = flip ? cw[w ^ 2] : cw[w];
-                        const uint32_t sw = flip ? s2[(w ^ 2) / 2] : s2[w / 2];
-                        uint32_t x[4];
-                        e2m1x8(word, x);
-                        const int chunk = 4 * (q & 1) + (w ^ flip);
-                        *reinterpret_cast<uint4*>(dst + t * 128 + ((chunk ^ (t & 7)) << 4)) =
-                            make_uint4(hmul2(x[0], sw), hmul2(x[1], sw), hmul2(x[2], sw), hmul2(x[3], sw));
-                    }
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t word = flip ? cw[w ^ 2] : cw[w];
+                    const uint32_t sw = flip ? s2[(w ^ 2) / 2] : s2[w / 2];
+                    uint32_t x[4];
+                    e2m1x8(word, x);
+                    const int chunk = 4 * (q & 1) + (w ^ flip);
+                    *reinterpret_cast<uint4*>(dst + t * 128 + ((chunk ^ (t & 7)) << 4)) =
+                        make_uint4(hmul2(x[0], sw), hmul2(x[1], sw), hmul2(x[2], sw), hmul2(x[3], sw));
                 }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&kv_full[slot]);
             }
-            if (ok && lane == 0) mbar_arrive(&raw_empty[rs]);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&kv_full[slot]);
+                mbar_arrive(&raw_empty[rs]);
+            }
         }
     } else {
         regs_down<kRegIssue>();
@@ -386,60 +407,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
                 return lane < GPT && j < n && tg < hi && tg + kGroup > lo;
             };
             auto page_of = [&](int j) { return wanted(j) ? tab[(tok0 + j * kTok + lane * kGroup) / P] : -1; };
-            int page = page_of(0), j = 0;
-            for (; j < n; ++j) {
-                const int rs = j % kRaw;
-                if (!__all_sync(0xffffffffu, wait_on(&raw_empty[rs], (j / kRaw + 1) & 1, dead))) break;
+            int page = page_of(0), next = page_of(1), seq = 0;
+            for (; seq < 2 * n; ++seq) {
+                const int rs = seq % kRaw, j = seq >> 1;
+                if (!__all_sync(0xffffffffu, wait_on(&raw_empty[rs], (seq / kRaw + 1) & 1, dead))) break;
                 const int tg = tok0 + j * kTok + lane * kGroup;
                 const bool want = wanted(j), ok = want && page >= 0 && page < a.c.num_pages;
                 if (want && !ok) set_status(a.status, KVQ_STATUS_BAD_PAGE);
                 const uint32_t v = __ballot_sync(0xffffffffu, ok);
                 if (lane == 0) {
                     gmask[j & 7] = (uint8_t)v;
-                    mbar_arrive_expect_tx(&raw_full[rs], __popc(v) * Paged<D>::kBytes);
+                    mbar_arrive_expect_tx(&raw_full[rs], __popc(v) * Paged<D>::kHalf);
                 }
                 __syncwarp();
                 if (ok)
-                    bulk_load(smem + L::raw + rs * L::raw_bytes + lane * Paged<D>::kBytes,
-                              a.pool + group_at(a.c, page, h, tg % P / kGroup), Paged<D>::kBytes, &raw_full[rs]);
-                page = page_of(j + 1);
+                    bulk_load(smem + L::raw + rs * L::raw_bytes + lane * Paged<D>::kHalf,
+                              a.pool + group_at(a.c, page, h, tg % P / kGroup) + (seq & 1) * Paged<D>::kHalf,
+                              Paged<D>::kHalf, &raw_full[rs]);
+                if (seq & 1) page = next, next = page_of(j + 2);
             }
             if (*dead)  // let the copies in flight land before the memory is left
-                for (int k = max(0, j - kRaw); k < j; ++k) mbar_wait(&raw_full[k % kRaw], (k / kRaw) & 1);
-        } else if (warp == 13 && lane == 0) {
+                for (int k = max(0, seq - kRaw); k < seq; ++k) mbar_wait(&raw_full[k % kRaw], (k / kRaw) & 1);
+        } else if (warp == 13 && elect_one()) {
             constexpr uint32_t is = mma_desc(kTok, false), io = mma_desc(D, true);
-            const uint32_t qa = smem_u32(smem + L::q), sa = smem_u32(smem + L::slot);
+            // an address enters a descriptor in units of 16 bytes, in its low bits
+            const uint64_t qd = smem_desc(smem_u32(smem + L::q), 16, 1024);
+            const uint64_t kd = smem_desc(smem_u32(smem + L::slot), 16, 1024);
+            const uint64_t vd = smem_desc(smem_u32(smem + L::slot), kTok * 128, 1024);
             auto scores = [&](int i, int slot) {
+                const uint64_t qi = qd + i * (128 * 128 / 16), ki = kd + slot * (L::slot_bytes / 16);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    mma_ss(tmem + i * 128,
-                           smem_desc(qa + (k / 4) * (kRows * 128) + i * (128 * 128) + (k % 4) * 32, 16, 1024),
-                           smem_desc(sa + slot * L::slot_bytes + (k / 4) * (kTok * 128) + (k % 4) * 32, 16, 1024), is, k > 0);
+                    mma_ss(tmem + i * 128, qi + ((k / 4) * (kRows * 128) + (k % 4) * 32) / 16,
+                           ki + ((k / 4) * (kTok * 128) + (k % 4) * 32) / 16, is, k > 0);
                 mma_commit(&s_full[i]);
+            };
+            auto values = [&](int i, int slot, int half, bool add) {
+                const uint64_t vi = vd + slot * (L::slot_bytes / 16);
+#pragma unroll
+                for (int k = 4 * half; k < 4 * half + 4; ++k)
+                    mma_ts(tmem + 256 + i * D, tmem + i * 128 + k * 8, vi + k * (2048 / 16), io, add || k > 0);
             };
             bool ok = n > 0 && wait_on(&kv_full[0], 0, dead);
             if (ok) {
                 fence_after();
                 for (int i = 0; i < nact; ++i) scores(i, 0);
-                mma_commit(&kv_empty[0]);
             }
             for (int j = 0; j < n && ok; ++j) {
                 const int vs = 2 * j + 1, ks = 2 * j + 2;
                 ok = wait_on(&kv_full[vs % kSlots], (vs / kSlots) & 1, dead);
-                if (ok && j + 1 < n) ok = wait_on(&kv_full[ks % kSlots], (ks / kSlots) & 1, dead);
                 for (int i = 0; i < nact && ok; ++i) {
-                    ok = wait_on(&p_full[i], j & 1, dead);
-                    if (!ok) break;
-                    fence_after();
-#pragma unroll
-                    for (int k = 0; k < kTok / 16; ++k)
-                        mma_ts(tmem + 256 + i * D, tmem + i * 128 + k * 8,
-                               smem_desc(sa + (vs % kSlots) * L::slot_bytes + k * 2048, kTok * 128, 1024), io, j > 0 || k > 0);
-                    mma_commit(&pv_done[i]);
-                    if (i == nact - 1) mma_commit(&kv_empty[vs % kSlots]);
-                    if (j + 1 < n) scores(i, ks % kSlots);
+                    for (int half = 0; half < 2 && ok; ++half) {
+                        ok = wait_on(&p_full[2 * i + half], j & 1, dead);
+                        fence_after();
+                        if (ok) values(i, vs % kSlots, half, j > 0);
+                    }
+                    if (j + 1 == n) {
+                        mma_commit(&pv_done[i]);
+                    } else if (ok) {
+                        if (i == 0) {
+                            ok = wait_on(&kv_full[ks % kSlots], (ks / kSlots) & 1, dead);
+                            fence_after();
+                            if (!ok) break;
+                        }
+                        scores(i, ks % kSlots);
+                    }
                 }
-                if (ok && j + 1 < n) mma_commit(&kv_empty[ks % kSlots]);
             }
             if (*dead) {  // products in flight end before the memory is given back
                 mma_commit(&s_full[0]);
