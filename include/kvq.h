@@ -581,7 +581,8 @@ int kvq_paged_dequantize(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache,
  *         outside [cu_q[0], cu_q[B]) are not touched
  *   max_q, max_len  host upper bounds on n_b and len[b]; queries and tokens past them are left
  *         out and set KVQ_STATUS_LEN_OVERFLOW
- *   splits  parts the token axis is cut into, 1 .. 256, or 0 for the library's choice
+ *   splits  about how many parts each request's tokens are cut into, 1 .. 256, or 0 for the
+ *           library's choice
  *   workspace  kvq_paged_attention_workspace bytes, 16-byte aligned (may be NULL when that is 0);
  *         calls that may run at the same time need workspaces of their own
  * The sums are taken in a fixed order: the same call returns the same bits.

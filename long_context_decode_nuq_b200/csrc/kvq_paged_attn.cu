@@ -7,10 +7,19 @@ using namespace kvq_host;
 namespace {
 
 // ---------------------------------------------------------------------------------
-// A block takes RB = 8 * NT query rows of one (request, kv head) -- row r is query r / G, head
-// r % G of the kv head's G -- and one split of the tokens they see.  Each warp walks tiles of 32
-// tokens of its own (a ring of bulk copies, a group of 16 tokens is one contiguous run of the
-// pool), keeps the running maximum and sum of its rows, and the block joins its warps at the end.
+// Few query rows per kv head (decode, drafts to verify): at most RB = 8 * NT of them, row r being
+// query r / G, head r % G of the kv head's G.
+//
+// The work is one line of units, 64 tokens of one (request, kv head) each, in request-major order;
+// block w of N takes units [w T / N, (w+1) T / N) of it, so every block has the same share whatever
+// the lengths are.  A (request, kv head) inside one block is finished there; one that a block
+// boundary cuts leaves (m, l, O) of each piece in the workspace, a block having at most two such
+// pieces, and k_paged_join adds them up in order, told by the block of the first piece where they
+// are.
+//
+// In a block one warp brings the codes: a stage is 32 tokens for each of the W others, a lane one
+// group of 16 tokens, which is one contiguous run of the pool.  The W warps take 32 tokens each,
+// keep running maxima and sums of the rows and join at the end of a piece.
 //
 // Both products run on the tensor cores with the tokens as the long side, so one m16n8k16
 // instruction serves 16 tokens for 8 rows and a single query head wastes only idle columns:
@@ -19,13 +28,13 @@ namespace {
 // significant bits and a size of 2^-10 .. 2688, so K and V enter exactly.  A bf16 query enters as
 // fp16 too: each row is divided by a power of two that puts its largest value at 2^10, which
 // leaves every value within 2^-35 of the row's largest exact.  Only P is rounded, to fp16 (half a
-// step is 2^-11); it is kept at up to 2^15 of the largest so that tokens 2^-26 below the maximum still have all
-// their bits.  Maximum, sums and O are binary32.
+// step is 2^-11); it is kept at up to 2^15 of the largest so that tokens 2^-26 below the maximum
+// still have all their bits.  Maximum, sums and O are binary32.
 //
 // The rows of a K tile are permuted (tau) so that both the 16-byte reads of K rows and the 8-byte
 // reads of V rows spread over the banks; S^T then leaves its lanes with (token, 2 rows), which
 // movmatrix turns into the B operand of the second product.
-constexpr int kTile = 32;
+constexpr int kUnit = 64;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -42,341 +51,531 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 template <int NT>
 struct Shape {
-    static constexpr int W = NT == 1 ? 8 : 4;   // warps
-    static constexpr int ST = NT == 1 ? 3 : 4;  // ring stages per warp
+    static constexpr int W = NT == 1 ? 7 : 5;   // warps that compute (8 and 6 with the loader)
+    static constexpr int ST = NT == 1 ? 2 : 3;  // stages
+    static constexpr int threads = W * 32 + 32;
 };
 template <int D, int NT>
-constexpr int attn_smem() {
-    constexpr int ring = Shape<NT>::W * Shape<NT>::ST * 2 * Paged<D>::kBytes;
-    constexpr int join = Shape<NT>::W * 8 * NT * (D + 4 + 2) * 4;
-    return (ring > join ? ring : join) + 8 * Shape<NT>::W * Shape<NT>::ST;
+struct FewSmem {
+    static constexpr int W = Shape<NT>::W, ST = Shape<NT>::ST, RB = 8 * NT;
+    static constexpr int stage = W * 2 * Paged<D>::kBytes;
+    static constexpr int joint = ST * stage;                  // float [W][RB][D + 4]
+    static constexpr int ml = joint + W * RB * (D + 4) * 4;   // float2 [W][RB]
+    static constexpr int bar = ml + W * RB * 8;               // full[ST], empty[ST]
+    static constexpr int misc = bar + 16 * ST;                // got[ST], dead, start
+    static constexpr int scan = misc + 64;                    // int64 [32]
+    static constexpr int total = scan + 32 * 8;
+};
+
+// What a request contributes: its rows, the tokens they see and its units (per kv head).
+struct Seg {
+    Rows rw;
+    int first;            // position of query 0 (negative: it sees nothing)
+    int lo, hi;           // tokens some row sees
+    int all_lo, all_hi;   // tokens every row sees
+    int tbase, u;
+};
+__device__ __forceinline__ Seg seg_of(const AttnArgs& a, int b) {
+    Seg s;
+    s.rw = rows_of(a, b);
+    s.first = s.rw.len - s.rw.n;
+    s.hi = min(s.rw.kv, s.first + s.rw.nq);
+    s.lo = a.window > 0 ? max(0, s.first + 1 - a.window) : 0;
+    s.all_hi = min(s.rw.kv, s.first + 1);
+    s.all_lo = a.window > 0 ? max(0, s.first + s.rw.nq - a.window) : 0;
+    s.tbase = s.lo & ~(kGroup - 1);
+    // one that sees nothing still has a unit, which writes its zeros
+    s.u = s.rw.R == 0 ? 0 : s.hi > s.lo ? (s.hi - s.tbase + kUnit - 1) / kUnit : 1;
+    return s;
+}
+
+// floor(T x / N), in 32 bits where they hold it (a 64-bit division costs a tenth of a microsecond).
+__device__ __forceinline__ int64_t share(int64_t T, int x, int N) {
+    if (T < (1 << 20) && x <= 4096) return (uint32_t)T * (uint32_t)x / (uint32_t)N;
+    return T * x / N;
+}
+
+// Wait for a phase, giving up where another warp has.
+__device__ __forceinline__ bool wait_or(uint64_t* bar, uint32_t parity, volatile int* dead) {
+    for (uint32_t it = 0; it < (1u << 22); ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 63u && *dead) return false;
+    }
+    *dead = 1;
+    return false;
 }
 
 template <int D, int NT, bool BF>
-__global__ void __launch_bounds__(Shape<NT>::W * 32, NT == 1 ? 2 : 1)
-    k_paged_attn(const AttnArgs a) {
-    constexpr int W = Shape<NT>::W, ST = Shape<NT>::ST, RB = 8 * NT;
+__global__ void __launch_bounds__(Shape<NT>::threads, 2) k_paged_attn(const AttnArgs a, int B) {
+    using L = FewSmem<D, NT>;
+    constexpr int W = L::W, ST = L::ST, RB = L::RB;
     constexpr int GB = Paged<D>::kBytes, HALF = Paged<D>::kHalf, ROW = Paged<D>::kRow, SC = Paged<D>::kScales;
     constexpr int KS = D / 16;  // k-steps of S^T, and 16-channel tiles of O^T
     constexpr int KW = D / 32;  // code words of a lane's part of a K row
     constexpr int VW = D / 64;  // code words of a lane's part of a V row
+    constexpr int STEP = W * 32;  // tokens of a stage
     extern __shared__ __align__(128) uint8_t smem[];
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bar);
+    uint64_t* empty = full + ST;
+    volatile uint32_t* s_got = reinterpret_cast<uint32_t*>(smem + L::misc);
+    volatile int* dead = reinterpret_cast<int*>(smem + L::misc + 16);
+    int64_t* s_start = reinterpret_cast<int64_t*>(smem + L::misc + 24);  // units before b0, b0, T
+    int64_t* s_scan = reinterpret_cast<int64_t*>(smem + L::scan);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int s = blockIdx.x % a.S, rb = blockIdx.x / a.S, h = blockIdx.y, b = blockIdx.z;
-    const int G = a.c.Hq / a.c.Hkv, P = a.c.page_tokens;
-    const Rows rw = rows_of(a, b);
-    const int r0 = rb * RB;
-    if (threadIdx.x == 0 && h == 0 && blockIdx.x == 0 && (rw.n > rw.nq || rw.len > rw.kv))
-        set_status(a.status, KVQ_STATUS_LEN_OVERFLOW);
-    if (r0 >= rw.R) return;
-    const int i0 = r0 / G, i1 = (min(r0 + RB, rw.R) - 1) / G;
-    const int first = rw.len - rw.n;  // position of query 0 (negative: it sees nothing)
-    const int hi = min(rw.kv, first + i1 + 1);
-    const int lo = a.window > 0 ? max(0, first + i0 + 1 - a.window) : 0;
-    const int all_hi = min(rw.kv, first + i0 + 1);  // tokens every row sees: [all_lo, all_hi)
-    const int all_lo = a.window > 0 ? max(0, first + i1 + 1 - a.window) : 0;
-    const int tbase = lo & ~(kTile - 1);
-    const int tiles = hi > lo ? (hi - tbase + kTile - 1) / kTile : 0;
-    const int te = (int)((int64_t)tiles * (s + 1) / a.S);
-    const int tb = (int)((int64_t)tiles * s / a.S) + warp;
+    const int G = a.c.Hq / a.c.Hkv, Hkv = a.c.Hkv;
+    const int lp = 31 - __clz(a.c.page_tokens);
 
-    uint8_t* ring = smem + warp * ST * 2 * GB;
-    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + attn_smem<D, NT>() - 8 * W * ST) + warp * ST;
-    if (lane == 0) {
-        for (int i = 0; i < ST; ++i) mbar_init(&bar[i], 1);
+    if (threadIdx.x == 0) {
+        *dead = 0;
+        for (int i = 0; i < ST; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], W);
         fence_mbar_init();
     }
-    __syncwarp();
-
-    // loader: lanes 0 and 1 each bring one group of a tile; a page number read one tile ahead
-    const int32_t* tab = a.table + (size_t)b * a.c.max_pages;
-    auto page_of = [&](int tile) {
-        const int tg = tbase + tile * kTile + lane * kGroup;
-        return lane < 2 && tile < te && tg < hi && tg + kGroup > lo ? tab[tg / P] : -1;
+    // where this block's units begin: prefix sums of the requests' units
+    int64_t base = 0, T;  // units before request b; all units
+    int b = 0;
+    auto report = [&](const Seg& s, int r) {  // by block 0, for every request
+        if (s.rw.n > s.rw.nq || s.rw.len > s.rw.kv) set_status(a.status, KVQ_STATUS_LEN_OVERFLOW);
+        if (s.u == 0 && a.rec && a.by_request)
+            for (int h = 0; h < Hkv; ++h) a.rec[r * Hkv + h] = make_int4(-1, 0, 0, 0);
     };
-    uint32_t have = 0;  // two bits a stage: groups that were brought
-    auto issue = [&](int stage, int tile, int page) {
-        const int tg = tbase + tile * kTile + lane * kGroup;
-        const bool want = lane < 2 && tile < te && tg < hi && tg + kGroup > lo;
-        const bool ok = want && page >= 0 && page < a.c.num_pages;
-        if (want && !ok) set_status(a.status, KVQ_STATUS_BAD_PAGE);
-        const uint32_t v = __ballot_sync(0xffffffffu, ok);
-        have = (have & ~(3u << (2 * stage))) | v << (2 * stage);
-        if (lane == 0) mbar_arrive_expect_tx(&bar[stage], __popc(v) * GB);
-        __syncwarp();
-        if (ok)
-            bulk_load(ring + (stage * 2 + lane) * GB, a.pool + group_at(a.c, page, h, tg % P / kGroup), GB, &bar[stage]);
-    };
-    int issued = 0;
-    for (; issued < ST && tb + issued * W < te; ++issued) issue(issued, tb + issued * W, page_of(tb + issued * W));
-    int next_page = page_of(tb + issued * W);
+    if (B <= 32) {  // a lane a request, every warp for itself
+        int u = 0;
+        if (lane < B) {
+            const Seg s = seg_of(a, lane);
+            u = s.u;
+            if (blockIdx.x == 0 && warp == 0) report(s, lane);
+        }
+        int64_t incl = u;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        T = __shfl_sync(0xffffffffu, incl, 31) * Hkv;
+        const int64_t at = share(T, blockIdx.x, (int)min((int64_t)gridDim.x, max(T, (int64_t)1)));
+        const uint32_t past = __ballot_sync(0xffffffffu, incl * Hkv > at);
+        b = past ? __ffs(past) - 1 : 0;
+        base = __shfl_sync(0xffffffffu, incl - u, b) * Hkv;
+        __syncthreads();
+    } else {  // a thread a run of requests
+        const int per = (B + Shape<NT>::threads - 1) / Shape<NT>::threads;
+        const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
+        int64_t mine = 0;
+        for (int r = b0; r < b1; ++r) {
+            const Seg s = seg_of(a, r);
+            mine += s.u;
+            if (blockIdx.x == 0) report(s, r);
+        }
+        int64_t incl = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) s_scan[warp] = incl;
+        __syncthreads();
+        int64_t total = 0;
+        for (int i = 0; i <= W; ++i) {
+            if (i < warp) incl += s_scan[i];
+            total += s_scan[i];
+        }
+        T = total * Hkv;
+        const int64_t at = share(T, blockIdx.x, (int)min((int64_t)gridDim.x, max(T, (int64_t)1)));
+        int64_t ub = incl - mine;  // units (per kv head) before request b0
+        if (ub * Hkv <= at && at < incl * Hkv) {
+            int r = b0;
+            for (;; ++r) {
+                const int u = seg_of(a, r).u;
+                if ((ub + u) * Hkv > at) break;
+                ub += u;
+            }
+            s_start[0] = ub * Hkv, s_start[1] = r;
+        }
+        __syncthreads();
+        if (at < T) base = s_start[0], b = (int)s_start[1];
+    }
+    // every block has started by the time this takes effect: k_paged_join may take free places
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int N = (int)min((int64_t)gridDim.x, T);  // blocks that have units
+    if ((int)blockIdx.x >= N) {
+        if (a.rec && !a.by_request && threadIdx.x == 0) a.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        return;
+    }
+    const int64_t g0 = share(T, blockIdx.x, N), g1 = share(T, blockIdx.x + 1, N);
+    Seg sg = seg_of(a, b);
 
-    // queries: lane (g, t) holds channels [t*D/4, (t+1)*D/4) of row g, as the columns of B
-    uint32_t qf[NT][KS][2];
-    float sl2[NT][2];
-    int pos[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int r = r0 + nt * 8 + g;
-        uint32_t w[KS * 2] = {};
-        if (r < rw.R) {
-            const uint16_t* src = a.q + (int64_t)(rw.c0 + r / G) * a.qs + (h * G + r % G) * D + t * (D / 4);
-#pragma unroll
-            for (int i = 0; i < KS / 2; ++i) {
-                const uint4 x = reinterpret_cast<const uint4*>(src)[i];
-                w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+    // the pieces of [g0, g1): request b, kv head h, units [u0, u0 + un)
+    int h = 0, u0 = 0, un = 0;
+    auto piece = [&](int64_t at) {
+        while (at >= base + (int64_t)sg.u * Hkv) {
+            base += (int64_t)sg.u * Hkv;
+            sg = seg_of(a, ++b);
+        }
+        const int64_t off = at - base;
+        h = off <= INT32_MAX ? (int)((uint32_t)off / (uint32_t)sg.u) : (int)(off / sg.u);
+        u0 = (int)(off - (int64_t)h * sg.u);
+        un = (int)min((int64_t)(sg.u - u0), g1 - at);
+    };
+
+    if (warp == W) {  // the loader
+        const size_t page_bytes = group_at(a.c, 1, 0, 0), head_bytes = (size_t)(a.c.page_tokens / kGroup) * GB;
+        int k = 0;
+        for (int64_t at = g0; at < g1 && !*dead; at += un) {
+            piece(at);
+            const int32_t* tab = a.table + (size_t)b * a.c.max_pages;
+            const uint8_t* pool = a.pool + h * head_bytes;
+            const int t0 = sg.tbase + u0 * kUnit, t1 = min(sg.hi, t0 + un * kUnit);
+            auto wanted = [&](int tok) { return lane < 2 * W && tok < t1 && tok + kGroup > sg.lo; };
+            int tg = t0 + lane * kGroup;
+            int page = wanted(tg) ? tab[tg >> lp] : -1;
+            for (int ts = t0; ts < t1; ts += STEP, tg += STEP, ++k) {
+                const int st = k % ST;
+                const bool want = wanted(tg), ok = want && page >= 0 && page < a.c.num_pages;
+                const int nxt = wanted(tg + STEP) ? tab[(tg + STEP) >> lp] : -1;
+                if (want && !ok) set_status(a.status, KVQ_STATUS_BAD_PAGE);
+                if (!__all_sync(0xffffffffu, wait_or(&empty[st], (k / ST + 1) & 1, dead))) break;
+                const uint32_t v = __ballot_sync(0xffffffffu, ok);
+                if (lane == 0) {
+                    s_got[st] = v;
+                    mbar_arrive_expect_tx(&full[st], __popc(v) * GB);
+                }
+                __syncwarp();
+                if (ok)
+                    bulk_load(smem + st * L::stage + lane * GB,
+                              pool + page * page_bytes + ((tg & (a.c.page_tokens - 1)) / kGroup) * GB, GB, &full[st]);
+                page = nxt;
             }
         }
-        int e = 0;
-        if (BF) {
-            uint32_t mx = 0;
-#pragma unroll
-            for (int i = 0; i < KS * 2; ++i) mx = __vmaxu2(mx, w[i] & 0x7fff7fffu);
-            mx = max(mx & 0xffffu, mx >> 16);
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const int eb = (int)(mx >> 7);
-            if (eb < 255) e = max(eb - 127 - 10, -120);
-            const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-            for (int i = 0; i < KS * 2; ++i) w[i] = pack_h2(lo16<true>(w[i]) * f, hi16<true>(w[i]) * f);
-        }
-#pragma unroll
-        for (int j = 0; j < KS; ++j) qf[nt][j][0] = w[2 * j], qf[nt][j][1] = w[2 * j + 1];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            const int er = __shfl_sync(0xffffffffu, e, (2 * t + z) * 4);
-            sl2[nt][z] = a.scale_log2 * __uint_as_float((uint32_t)(127 + er) << 23);
-            pos[nt][z] = first + (r0 + nt * 8 + 2 * t + z) / G;
-        }
+        if (*dead)  // a copy did not come: let the others land before the memory is left
+            for (int i = max(0, k - ST); i < k; ++i) mbar_wait(&full[i % ST], (i / ST) & 1);
+        return;
     }
 
-    float o[NT][KS][4] = {}, m[NT][2], l[NT][2] = {};
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
     const int tau = (g & 1) ? 4 + ((g >> 1) ^ 1) : (g >> 1);
     const int tv[4] = {t, 4 + (t ^ 1), 8 + t, 12 + (t ^ 1)};
-    bool dead = false;
-
+    float* so = reinterpret_cast<float*>(smem + L::joint);
+    float2* sml = reinterpret_cast<float2*>(smem + L::ml);
     int k = 0;
-    for (int tile = tb; tile < te; tile += W, ++k) {
-        const int stage = k % ST;
-        dead = !__all_sync(0xffffffffu, mbar_wait(&bar[stage], (k / ST) & 1));
-        if (dead) break;
-        const uint8_t* buf = ring + stage * 2 * GB;
-        const int t0 = tbase + tile * kTile;
-        const uint32_t got = have >> (2 * stage) & 3u;
-        const bool mask = got != 3u || t0 + kTile > all_hi || t0 < all_lo;
-
-        float sc[2][NT][4];
-#pragma unroll
-        for (int gr = 0; gr < 2; ++gr) {
-            const uint8_t* kb = buf + gr * GB;
-            uint32_t kc[2][KW];
-            uint32_t ks[2][(D + 127) / 128 * 2];  // scale pairs (s, s) of the lane's channels
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                const uint8_t* row = kb + (tau + 8 * z) * ROW + t * (D / 8);
-                const uint8_t* srow = kb + kGroup * ROW + (tau + 8 * z) * SC;
-                if constexpr (D == 128) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(row);
-                    kc[z][0] = x.x, kc[z][1] = x.y, kc[z][2] = x.z, kc[z][3] = x.w;
-                    const uint32_t two = e4m3x2(*reinterpret_cast<const uint16_t*>(srow + 2 * t));
-                    ks[z][0] = __byte_perm(two, 0, 0x1010);
-                    ks[z][1] = __byte_perm(two, 0, 0x3232);
-                } else {
-                    const uint2 x = *reinterpret_cast<const uint2*>(row);
-                    kc[z][0] = x.x, kc[z][1] = x.y;
-                    const uint32_t one = srow[t];
-                    ks[z][0] = ks[z][1] = e4m3x2(one | one << 8);
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) sc[gr][nt][z] = 0.0f;
-#pragma unroll
-            for (int w = 0; w < KW; ++w) {
-                uint32_t x0[4], x1[4];
-                e2m1x8(kc[0][w], x0);
-                e2m1x8(kc[1][w], x1);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint32_t s0 = ks[0][w * 2 / KW], s1 = ks[1][w * 2 / KW];
-                    const uint32_t A[4] = {hmul2(x0[2 * u], s0), hmul2(x1[2 * u], s1),
-                                           hmul2(x0[2 * u + 1], s0), hmul2(x1[2 * u + 1], s1)};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16816(sc[gr][nt], A, qf[nt][2 * w + u][0], qf[nt][2 * w + u][1]);
-                }
-            }
-        }
-        // scores in the log2 domain; masked ones are -inf
-        float tm[NT][2];
+    for (int64_t at = g0; at < g1; at += un) {
+        piece(at);
+        const Rows& rw = sg.rw;
+        // queries: lane (g, t) holds channels [t*D/4, (t+1)*D/4) of row g, as the columns of B
+        uint32_t qf[NT][KS][2];
+        float sl2[NT][2];
+        int pos[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            tm[nt][0] = tm[nt][1] = -INFINITY;
+            const int r = nt * 8 + g;
+            uint32_t w[KS * 2] = {};
+            if (r < rw.R) {
+                const uint16_t* src = a.q + (int64_t)(rw.c0 + r / G) * a.qs + (h * G + r % G) * D + t * (D / 4);
 #pragma unroll
-            for (int gr = 0; gr < 2; ++gr)
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    float x = sc[gr][nt][z] * sl2[nt][z & 1];
-                    if (mask) {
-                        const int tok = t0 + gr * kGroup + tau + (z & 2) * 4;
-                        const int p = pos[nt][z & 1];
-                        const bool see = (got >> gr & 1u) && tok < rw.kv && tok <= p &&
-                                         (a.window <= 0 || tok > p - a.window);
-                        if (!see) x = -INFINITY;
-                    }
-                    sc[gr][nt][z] = x;
-                    tm[nt][z & 1] = fmaxf(tm[nt][z & 1], x);
+                for (int i = 0; i < KS / 2; ++i) {
+                    const uint4 x = reinterpret_cast<const uint4*>(src)[i];
+                    w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
                 }
-        }
-        bool grow = false;
+            }
+            // a negative scale goes into the query, so that the largest score is the largest product
+            const uint32_t neg = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int i = 0; i < KS * 2; ++i) w[i] ^= neg;
+            int e = 0;
+            if (BF) {
+                uint32_t mx = 0;
+#pragma unroll
+                for (int i = 0; i < KS * 2; ++i) mx = __vmaxu2(mx, w[i] & 0x7fff7fffu);
+                mx = max(mx & 0xffffu, mx >> 16);
+                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const int eb = (int)(mx >> 7);
+                if (eb < 255) e = max(eb - 127 - 10, -120);
+                const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+                for (int i = 0; i < KS * 2; ++i) w[i] = pack_h2(lo16<true>(w[i]) * f, hi16<true>(w[i]) * f);
+            }
+#pragma unroll
+            for (int j = 0; j < KS; ++j) qf[nt][j][0] = w[2 * j], qf[nt][j][1] = w[2 * j + 1];
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
-                tm[nt][z] = fmaxf(tm[nt][z], __shfl_xor_sync(0xffffffffu, tm[nt][z], 4));
-                tm[nt][z] = fmaxf(tm[nt][z], __shfl_xor_sync(0xffffffffu, tm[nt][z], 8));
-                tm[nt][z] = fmaxf(tm[nt][z], __shfl_xor_sync(0xffffffffu, tm[nt][z], 16));
-                grow |= tm[nt][z] - m[nt][z] > kPRoom;
+                const int er = __shfl_sync(0xffffffffu, e, (2 * t + z) * 4);
+                sl2[nt][z] = fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + er) << 23), 1e-37f);
+                pos[nt][z] = sg.first + (nt * 8 + 2 * t + z) / G;
             }
-        if (__any_sync(0xffffffffu, grow)) {
+        }
+
+        float o[NT][KS][4] = {}, m[NT][2], l[NT][2] = {};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
+        const int ts0 = sg.tbase + u0 * kUnit, ts1 = min(sg.hi, ts0 + un * kUnit);
+        for (int ts = ts0; ts < ts1; ts += STEP, ++k) {
+            const int stage = k % ST, t0 = ts + warp * 32;
+            if (!__all_sync(0xffffffffu, wait_or(&full[stage], (k / ST) & 1, dead))) break;
+            const uint32_t got = s_got[stage] >> (2 * warp) & 3u;
+            if (t0 >= ts1) {
+                if (lane == 0) mbar_arrive(&empty[stage]);
+                continue;
+            }
+            const uint8_t* buf = smem + stage * L::stage + warp * 2 * GB;
+            const bool mask = got != 3u || t0 + 32 > sg.all_hi || t0 < sg.all_lo;
+
+            float sc[2][NT][4];
+#pragma unroll
+            for (int gr = 0; gr < 2; ++gr) {
+                const uint8_t* kb = buf + gr * GB;
+                uint32_t kc[2][KW];
+                uint32_t ks[2][2];  // scale pairs (s, s) of the lane's channels
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const uint8_t* row = kb + (tau + 8 * z) * ROW + t * (D / 8);
+                    const uint8_t* srow = kb + kGroup * ROW + (tau + 8 * z) * SC;
+                    if constexpr (D == 128) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(row);
+                        kc[z][0] = x.x, kc[z][1] = x.y, kc[z][2] = x.z, kc[z][3] = x.w;
+                        const uint32_t two = e4m3x2(*reinterpret_cast<const uint16_t*>(srow + 2 * t));
+                        ks[z][0] = __byte_perm(two, 0, 0x1010);
+                        ks[z][1] = __byte_perm(two, 0, 0x3232);
+                    } else {
+                        const uint2 x = *reinterpret_cast<const uint2*>(row);
+                        kc[z][0] = x.x, kc[z][1] = x.y;
+                        const uint32_t one = srow[t];
+                        ks[z][0] = ks[z][1] = e4m3x2(one | one << 8);
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) sc[gr][nt][z] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < KW; ++w) {
+                    uint32_t x0[4], x1[4];
+                    e2m1x8(kc[0][w], x0);
+                    e2m1x8(kc[1][w], x1);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t s0 = ks[0][w * 2 / KW], s1 = ks[1][w * 2 / KW];
+                        const uint32_t A[4] = {hmul2(x0[2 * u], s0), hmul2(x1[2 * u], s1),
+                                               hmul2(x0[2 * u + 1], s0), hmul2(x1[2 * u + 1], s1)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816(sc[gr][nt], A, qf[nt][2 * w + u][0], qf[nt][2 * w + u][1]);
+                    }
+                }
+            }
+            if (mask) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const int tok = t0 + gr * kGroup + tau + (z & 2) * 4;
+                            const int p = pos[nt][z & 1];
+                            const bool see = (got >> gr & 1u) && tok < ts1 && tok <= p && (a.window <= 0 || tok > p - a.window);
+                            if (!see) sc[gr][nt][z] = -INFINITY;
+                        }
+            }
+            // the maximum moves only when some lane's scores ask for it, so the common case needs
+            // no exchange between lanes
+            float tm[NT][2];
+            bool grow = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
-                    const float mn = fmaxf(m[nt][z], tm[nt][z] - kPShift);
-                    const float al = m[nt][z] == mn ? 1.0f : ex2(m[nt][z] - mn);
-                    m[nt][z] = mn;
-                    l[nt][z] *= al;
-#pragma unroll
-                    for (int j = 0; j < KS; ++j) o[nt][j][z] *= al, o[nt][j][z + 2] *= al;
+                    tm[nt][z] = fmaxf(fmaxf(sc[0][nt][z], sc[0][nt][z + 2]), fmaxf(sc[1][nt][z], sc[1][nt][z + 2])) * sl2[nt][z];
+                    grow |= tm[nt][z] - m[nt][z] > kPRoom;
                 }
-        }
-        uint32_t pf[2][NT][2];
+            if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const float m0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0];
-            const float m1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        float x = tm[nt][z];
+#pragma unroll
+                        for (int y = 4; y < 32; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
+                        const float mn = fmaxf(m[nt][z], x - kPShift);
+                        const float al = m[nt][z] == mn ? 1.0f : ex2(m[nt][z] - mn);
+                        m[nt][z] = mn;
+                        l[nt][z] *= al;
+#pragma unroll
+                        for (int j = 0; j < KS; ++j) o[nt][j][z] *= al, o[nt][j][z + 2] *= al;
+                    }
+            }
+            uint32_t pf[2][NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float m0 = m[nt][0] == -INFINITY ? 0.0f : -m[nt][0];
+                const float m1 = m[nt][1] == -INFINITY ? 0.0f : -m[nt][1];
+#pragma unroll
+                for (int gr = 0; gr < 2; ++gr) {
+                    const float p0 = ex2(fmaf(sc[gr][nt][0], sl2[nt][0], m0)), p1 = ex2(fmaf(sc[gr][nt][1], sl2[nt][1], m1));
+                    const float p2 = ex2(fmaf(sc[gr][nt][2], sl2[nt][0], m0)), p3 = ex2(fmaf(sc[gr][nt][3], sl2[nt][1], m1));
+                    l[nt][0] += p0 + p2;
+                    l[nt][1] += p1 + p3;
+                    pf[gr][nt][0] = transpose8x8(pack_h2(p0, p1));
+                    pf[gr][nt][1] = transpose8x8(pack_h2(p2, p3));
+                }
+            }
 #pragma unroll
             for (int gr = 0; gr < 2; ++gr) {
-                const float p0 = ex2(sc[gr][nt][0] - m0), p1 = ex2(sc[gr][nt][1] - m1);
-                const float p2 = ex2(sc[gr][nt][2] - m0), p3 = ex2(sc[gr][nt][3] - m1);
-                l[nt][0] += p0 + p2;
-                l[nt][1] += p1 + p3;
-                pf[gr][nt][0] = transpose8x8(pack_h2(p0, p1));
-                pf[gr][nt][1] = transpose8x8(pack_h2(p2, p3));
-            }
-        }
+                const uint8_t* vb = buf + gr * GB + HALF;
+                const uint8_t* vs = vb + kGroup * ROW + g * (D / 8) / kGroup;
+                uint32_t sb[4];
 #pragma unroll
-        for (int gr = 0; gr < 2; ++gr) {
-            const uint8_t* vb = buf + gr * GB + HALF;
-            const uint8_t* vs = vb + kGroup * ROW + g * (D / 8) / kGroup;
-            uint32_t sb[4];
+                for (int z = 0; z < 4; ++z) sb[z] = vs[tv[z] * SC];
+                if (mask) {
+                    // bytes nobody wrote may hold a NaN scale, and 0 * NaN is not 0
+                    const int tg = t0 + gr * kGroup;
 #pragma unroll
-            for (int z = 0; z < 4; ++z) sb[z] = vs[tv[z] * SC];
-            if (mask) {
-                // bytes nobody wrote may hold a NaN scale, and 0 * NaN is not 0
-                const int tg = t0 + gr * kGroup;
+                    for (int z = 0; z < 4; ++z)
+                        if (!(got >> gr & 1u) || tg + tv[z] >= rw.kv) sb[z] = 0;
+                }
+                const uint32_t s01 = e4m3x2(sb[0] | sb[1] << 8), s23 = e4m3x2(sb[2] | sb[3] << 8);
+                uint32_t vc[4][VW];
 #pragma unroll
-                for (int z = 0; z < 4; ++z)
-                    if (!(got >> gr & 1u) || tg + tv[z] >= rw.kv) sb[z] = 0;
-            }
-            const uint32_t s01 = e4m3x2(sb[0] | sb[1] << 8), s23 = e4m3x2(sb[2] | sb[3] << 8);
-            uint32_t vc[4][VW];
+                for (int z = 0; z < 4; ++z) {
+                    const uint8_t* row = vb + tv[z] * ROW + g * (D / 16);
+                    if constexpr (D == 128) {
+                        const uint2 x = *reinterpret_cast<const uint2*>(row);
+                        vc[z][0] = x.x, vc[z][1] = x.y;
+                    } else {
+                        vc[z][0] = *reinterpret_cast<const uint32_t*>(row);
+                    }
+                }
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const uint8_t* row = vb + tv[z] * ROW + g * (D / 16);
-                if constexpr (D == 128) {
-                    const uint2 x = *reinterpret_cast<const uint2*>(row);
-                    vc[z][0] = x.x, vc[z][1] = x.y;
-                } else {
-                    vc[z][0] = *reinterpret_cast<const uint32_t*>(row);
+                for (int w = 0; w < VW; ++w) {
+                    // bytes of (token a, token b) codes of one channel: even channels, then odd ones
+                    uint32_t e01[4], o01[4], e23[4], o23[4];
+                    e2m1x8((vc[0][w] & 0x0f0f0f0fu) | (vc[1][w] << 4 & 0xf0f0f0f0u), e01);
+                    e2m1x8((vc[0][w] >> 4 & 0x0f0f0f0fu) | (vc[1][w] & 0xf0f0f0f0u), o01);
+                    e2m1x8((vc[2][w] & 0x0f0f0f0fu) | (vc[3][w] << 4 & 0xf0f0f0f0u), e23);
+                    e2m1x8((vc[2][w] >> 4 & 0x0f0f0f0fu) | (vc[3][w] & 0xf0f0f0f0u), o23);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t A[4] = {hmul2(e01[i], s01), hmul2(o01[i], s01),
+                                               hmul2(e23[i], s23), hmul2(o23[i], s23)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816(o[nt][4 * w + i], A, pf[gr][nt][0], pf[gr][nt][1]);
+                    }
                 }
             }
-#pragma unroll
-            for (int w = 0; w < VW; ++w) {
-                // bytes of (token a, token b) codes of one channel: even channels, then odd ones
-                uint32_t e01[4], o01[4], e23[4], o23[4];
-                e2m1x8((vc[0][w] & 0x0f0f0f0fu) | (vc[1][w] << 4 & 0xf0f0f0f0u), e01);
-                e2m1x8((vc[0][w] >> 4 & 0x0f0f0f0fu) | (vc[1][w] & 0xf0f0f0f0u), o01);
-                e2m1x8((vc[2][w] & 0x0f0f0f0fu) | (vc[3][w] << 4 & 0xf0f0f0f0u), e23);
-                e2m1x8((vc[2][w] >> 4 & 0x0f0f0f0fu) | (vc[3][w] & 0xf0f0f0f0u), o23);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t A[4] = {hmul2(e01[i], s01), hmul2(o01[i], s01),
-                                           hmul2(e23[i], s23), hmul2(o23[i], s23)};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16816(o[nt][4 * w + i], A, pf[gr][nt][0], pf[gr][nt][1]);
-                }
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[stage]);
         }
-        __syncwarp();
-        if (tile + ST * W < te) {
-            issue(stage, tile + ST * W, next_page);
-            next_page = page_of(tile + (ST + 1) * W);
-            ++issued;
-        }
-    }
-    if (dead) {  // a copy did not come: say so, and let the others land before the memory is left
-        set_status(a.status, KVQ_STATUS_WAIT_TIMEOUT);
-        drain_chunks(bar, k, issued, ST);
-    }
 
-    // join the warps: rows' (m, l) and O through shared memory
+        // join the warps: rows' (m, l) and O through shared memory
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int z = 0; z < 2; ++z)
+            for (int z = 0; z < 2; ++z) {
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) l[nt][z] += __shfl_xor_sync(0xffffffffu, l[nt][z], x);
-    __syncthreads();
-    float* so = reinterpret_cast<float*>(smem);  // [W][RB][D + 4]
-    float2* sml = reinterpret_cast<float2*>(so + W * RB * (D + 4));  // [W][RB]
+                for (int x = 4; x < 32; x <<= 1) l[nt][z] += __shfl_xor_sync(0xffffffffu, l[nt][z], x);
+                const int row = nt * 8 + 2 * t + z;
+                float* dst = so + (warp * RB + row) * (D + 4) + g * (D / 8);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            const int row = nt * 8 + 2 * t + z;
-            float* dst = so + (warp * RB + row) * (D + 4) + g * (D / 8);
-#pragma unroll
-            for (int j = 0; j < KS; j += 2)  // tiles j: channels 2j, 2j + 1 of the lane's D/8
-                *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(o[nt][j][z], o[nt][j][z + 2], o[nt][j + 1][z], o[nt][j + 1][z + 2]);
-            if (g == 0) sml[warp * RB + row] = make_float2(m[nt][z], l[nt][z]);
+                for (int j = 0; j < KS; j += 2)  // tiles j: channels 2j, 2j + 1 of the lane's D/8
+                    *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(o[nt][j][z], o[nt][j][z + 2], o[nt][j + 1][z], o[nt][j + 1][z + 2]);
+                if (g == 0) sml[warp * RB + row] = make_float2(m[nt][z], l[nt][z]);
+            }
+        asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
+        const bool whole = un == sg.u;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (at != g0);
+        // the first piece says where all are: its slot, the block of the last one, and whose rows
+        if (a.rec && threadIdx.x == 0) {
+            int4 rec = make_int4(-1, 0, 0, 0);
+            if (u0 == 0 && !whole) {
+                const int64_t end = at + sg.u;
+                rec = make_int4((int)((end * N - 1) / T), (int)slot, rw.c0, h << 8 | rw.R);
+            }
+            if (a.by_request) {
+                if (u0 == 0) a.rec[b * Hkv + h] = rec;
+            } else if (rec.x >= 0 || at + un >= g1) {  // only a block's last piece can be one
+                a.rec[blockIdx.x] = rec;
+            }
         }
-    __syncthreads();
-    const int64_t nrow = (int64_t)a.total_q * a.c.Hq;
-    for (int it = threadIdx.x; it < RB * (D / 4); it += W * 32) {
-        const int row = it / (D / 4), c4 = it % (D / 4) * 4, r = r0 + row;
-        if (r >= rw.R) break;
-        float M = -INFINITY, L = 0.0f;
+        for (int it = threadIdx.x; it < RB * (D / 4); it += W * 32) {
+            const int row = it / (D / 4), c4 = it % (D / 4) * 4;
+            if (row >= rw.R) break;
+            float M = -INFINITY, LL = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) M = fmaxf(M, sml[w * RB + row].x);
-        float4 acc = make_float4(0, 0, 0, 0);
+            for (int w = 0; w < W; ++w) M = fmaxf(M, sml[w * RB + row].x);
+            float4 acc = make_float4(0, 0, 0, 0);
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const float2 ml = sml[w * RB + row];
-            const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - M);
-            const float4 x = *reinterpret_cast<const float4*>(so + (w * RB + row) * (D + 4) + c4);
-            L += f * ml.y;
-            acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+            for (int w = 0; w < W; ++w) {
+                const float2 ml = sml[w * RB + row];
+                if (ml.y == 0.0f) continue;  // saw nothing; a row of NaN scores has m = -inf, l = NaN
+                const float f = ex2(ml.x - M);
+                const float4 x = *reinterpret_cast<const float4*>(so + (w * RB + row) * (D + 4) + c4);
+                LL += f * ml.y;
+                acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+            }
+            if (whole) {
+                const int64_t grow = (int64_t)(rw.c0 + row / G) * a.c.Hq + h * G + row % G;
+                const float inv = LL == 0.0f ? 0.0f : a.out_scale / LL;
+                store4<BF>(a.out + grow * D + c4, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+                if (c4 == 0 && a.lse) a.lse[grow] = LL == 0.0f ? -INFINITY : (M + log2f(LL)) * kLn2;
+            } else {
+                *reinterpret_cast<float4*>(a.part + (slot * RB + row) * D + c4) = acc;
+                if (c4 == 0) a.pml[slot * RB + row] = make_float2(M, LL);
+            }
         }
-        const int64_t grow = (int64_t)(rw.c0 + r / G) * a.c.Hq + h * G + r % G;
-        if (a.S == 1) {
-            const float inv = L == 0.0f ? 0.0f : a.out_scale / L;
-            store4<BF>(a.out + grow * D + c4, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-            if (c4 == 0 && a.lse) a.lse[grow] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
-        } else {
-            *reinterpret_cast<float4*>(a.part + (s * nrow + grow) * D + c4) = acc;
-            if (c4 == 0) a.pml[s * nrow + grow] = make_float2(M, L);
-        }
+        asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
     }
+    if (threadIdx.x == 0 && *dead) set_status(a.status, KVQ_STATUS_WAIT_TIMEOUT);
 }
 
-// Joins the splits of a row, in split order: a warp per row.
+// Joins what block boundaries cut: block (x, row) takes record x, and adds its pieces in order of
+// their blocks, eight apart per warp and then over the warps.
+constexpr int kJoinWarps = 8;
+template <int D, bool BF>
+__global__ void __launch_bounds__(kJoinWarps * 32) k_paged_join(const AttnArgs a, int RB) {
+    __shared__ float s_o[kJoinWarps][D];
+    __shared__ float2 s_ml[kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 rec = a.rec[blockIdx.x];
+    const int w1 = rec.x, w0 = rec.y >> 1, h = rec.w >> 8, R = rec.w & 255;
+    if (w1 < 0 || row >= R) return;
+    constexpr int V = D / 32;
+    float acc[V] = {}, M = -INFINITY, L = 0.0f;
+#pragma unroll 4
+    for (int w = w0 + warp; w <= w1; w += kJoinWarps) {
+        const int64_t at = (w == w0 ? (int64_t)rec.y : 2 * (int64_t)w) * RB + row;
+        const float2 ml = a.pml[at];
+        float x[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = a.part[at * D + lane * V + i];
+        const float mn = fmaxf(M, ml.x);
+        // l = 0: saw nothing, m = -inf; a row of NaN scores has m = -inf, l = NaN
+        const float f = L == 0.0f ? 0.0f : ex2(M - mn), e = ml.y == 0.0f ? 0.0f : ex2(ml.x - mn);
+        L = L * f + e * ml.y;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = acc[i] * f + e * x[i];
+        M = mn;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) s_o[warp][lane * V + i] = acc[i];
+    if (lane == 0) s_ml[warp] = make_float2(M, L);
+    __syncthreads();
+    if (threadIdx.x >= D / 2) return;
+    M = -INFINITY, L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_ml[w].x);
+    float o0 = 0.0f, o1 = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        if (s_ml[w].y == 0.0f) continue;
+        const float f = ex2(s_ml[w].x - M);
+        L += f * s_ml[w].y;
+        o0 += f * s_o[w][2 * threadIdx.x], o1 += f * s_o[w][2 * threadIdx.x + 1];
+    }
+    const int G = a.c.Hq / a.c.Hkv;
+    const int64_t grow = (int64_t)(rec.z + row / G) * a.c.Hq + h * G + row % G;
+    const float inv = L == 0.0f ? 0.0f : a.out_scale / L;
+    reinterpret_cast<uint32_t*>(a.out + grow * D)[threadIdx.x] = pack16<BF>(o0 * inv, o1 * inv);
+    if (threadIdx.x == 0 && a.lse) a.lse[grow] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+// Joins the chunk kernel's splits of a row, in split order: a warp per row.
 constexpr int kMergeWarps = 4;
 template <int D, bool BF>
 __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const AttnArgs a) {
@@ -410,15 +609,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const AttnArgs
 }
 
 // ---------------------------------------------------------------------------------
-// Host: which kernel, rows per block, splits.
+// Host: which kernel, blocks or splits, workspace.
 struct Plan {
-    int nt;  // 8-row tiles of a block of k_paged_attn; 0: the chunk kernel
-    int nrb, S;
+    int nt;   // 8-row tiles of k_paged_attn; 0: the chunk kernel
+    int nrb;  // chunk kernel: row blocks
+    int S;    // chunk kernel: splits;  k_paged_attn: blocks
+    bool join;
 };
 
 constexpr int kSms = 148;
 // More rows of a kv head than this go to the chunk kernel.
-constexpr int kFewRows = 32;
+constexpr int kFewRows = 16;
 
 // Splits of the chunk kernel: the least time of a model in which a block costs 6 us and 1.2 us per
 // 128 tokens, blocks run one per SM in waves, and a split writes and reads its part at 5 TB/s.
@@ -434,40 +635,69 @@ int chunk_splits(const kvq_paged_cfg* c, int64_t units, int64_t tiles) {
     return best;
 }
 
-int splits_of(const kvq_paged_cfg* c, const Plan& p, int B, int64_t span) {
-    const int64_t units = (int64_t)B * c->Hkv * p.nrb;
-    if (p.nt == 0) return chunk_splits(c, units, (span + 127) / 128);
-    // the tokens a row block can see bound the useful splits at a tile a warp
-    const int warps = p.nt == 1 ? 8 : 4;
-    const int64_t tiles = (span + kTile - 1) / kTile;
-    int64_t S = (kSms * 4 + units - 1) / units;
-    const int64_t most = (tiles + warps - 1) / warps;
-    if (S > most) S = most;
-    return (int)(S > 256 ? 256 : S < 1 ? 1 : S);
-}
-
 Plan plan_of(const kvq_paged_cfg* c, int B, int max_q, int max_len, int splits, int window) {
     const int64_t R = (int64_t)max_q * (c->Hq / c->Hkv);
+    // no row block sees more tokens than this
+    int64_t span = max_len;
+    if (window > 0 && span > (int64_t)window + max_q + 128) span = (int64_t)window + max_q + 128;
     Plan p;
-    p.nt = R <= 8 ? 1 : R <= 16 ? 2 : R <= kFewRows ? 4 : 0;
-    const int rows = p.nt ? 8 * p.nt : kChunkRows;
-    p.nrb = (int)((R + rows - 1) / rows);
-    p.S = splits ? splits : splits_of(c, p, B, max_len);
-    if (!splits && window > 0 && max_len > (int64_t)window + max_q + 128) {
-        // a window only lowers the splits: the workspace is sized without it
-        const int S = splits_of(c, p, B, (int64_t)window + max_q + 128);
-        if (S < p.S) p.S = S;
+    p.nt = R <= 8 ? 1 : R <= kFewRows ? 2 : 0;
+    p.nrb = p.nt ? 1 : (int)((R + kChunkRows - 1) / kChunkRows);
+    const int64_t units = (int64_t)B * c->Hkv * p.nrb;
+    if (p.nt == 0) {
+        p.S = splits ? splits : chunk_splits(c, units, (span + 127) / 128);
+        // the workspace is sized without the window, which must not raise the splits
+        if (!splits && span < max_len) {
+            const int S = chunk_splits(c, units, ((int64_t)max_len + 127) / 128);
+            if (S < p.S) p.S = S;
+        }
+        p.join = p.S > 1;
+        return p;
     }
+    // two blocks are resident on an SM: one wave of equal shares, or fewer where there are not
+    // that many units of 64 tokens
+    const int64_t most = units * ((span + kUnit - 1) / kUnit + 1);
+    int64_t N = splits ? units * splits : 2 * kSms;
+    if (N > most) N = most;
+    p.S = (int)(N > (1 << 20) ? 1 << 20 : N);
+    p.join = span > kUnit && !(splits == 1 && B == 1);
     return p;
 }
 
-using AttnKernel = void (*)(AttnArgs);
+// Records of k_paged_attn for k_paged_join: one per (request, kv head), or per block if those are
+// fewer.
+int64_t records(const kvq_paged_cfg* cfg, const Plan& p, int32_t B) {
+    const int64_t segs = (int64_t)B * cfg->Hkv;
+    return segs < p.S ? segs : p.S;
+}
 
-template <int D, bool BF>
-AttnKernel attn_kernel(int nt, int* smem, int* warps) {
-    *warps = nt == 1 ? 8 : 4;
-    *smem = nt == 1 ? attn_smem<D, 1>() : nt == 2 ? attn_smem<D, 2>() : attn_smem<D, 4>();
-    return nt == 1 ? k_paged_attn<D, 1, BF> : nt == 2 ? k_paged_attn<D, 2, BF> : k_paged_attn<D, 4, BF>;
+size_t ws_bytes(const kvq_paged_cfg* cfg, const Plan& p, int32_t B, int32_t total_q) {
+    if (!p.join) return 0;
+    if (p.nt == 0) return (size_t)p.S * total_q * cfg->Hq * (cfg->D + 2) * 4;
+    return (size_t)(2 * p.S) * 8 * p.nt * (cfg->D + 2) * 4 + (size_t)records(cfg, p, B) * 16;
+}
+
+// Few rows: the main kernel, and the join where a (request, kv head) may have been cut.
+template <int D, int NT, bool BF>
+int run_few(const AttnArgs& a, const Plan& p, int B, int rows, cudaStream_t st) {
+    using L = FewSmem<D, NT>;
+    auto* kern = k_paged_attn<D, NT, BF>;
+    static SmemOptIn opt;
+    if (int e = opt.set((const void*)kern, L::total)) return e;
+    kern<<<p.S, Shape<NT>::threads, L::total, st>>>(a, B);
+    cudaError_t ce = cudaGetLastError();
+    if (ce || !p.join || p.S == 1) return record_cuda(ce);
+    // its launch overlaps the main kernel's end; it waits for that before it reads anything
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)records(&a.c, p, B), rows);
+    lc.blockDim = dim3(kJoinWarps * 32);
+    lc.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    return record_cuda(cudaLaunchKernelEx(&lc, k_paged_join<D, BF>, (const AttnArgs)a, L::RB));
 }
 
 int check_sizes(const kvq_paged_cfg* cfg, int32_t B, int32_t total_q, int32_t max_q,
@@ -476,12 +706,6 @@ int check_sizes(const kvq_paged_cfg* cfg, int32_t B, int32_t total_q, int32_t ma
         return KVQ_ERR_SHAPE;
     if (splits < 0 || splits > 256) return KVQ_ERR_RANGE;
     return KVQ_OK;
-}
-
-// The workspace is sized without the window, which only lowers the splits the library chooses.
-size_t ws_bytes(const kvq_paged_cfg* cfg, const Plan& p, int32_t total_q) {
-    if (p.S == 1) return 0;
-    return (size_t)p.S * total_q * cfg->Hq * (cfg->D + 2) * 4;
 }
 
 }  // namespace
@@ -494,7 +718,7 @@ int kvq_paged_attention_workspace(const kvq_paged_cfg* cfg, int32_t B, int32_t t
     if (e) return e;
     if (!bytes) return KVQ_ERR_NULL;
     if ((e = check_sizes(cfg, B, total_q, max_q, max_len, splits))) return e;
-    *bytes = ws_bytes(cfg, plan_of(cfg, B, max_q, max_len, splits, 0), total_q);
+    *bytes = ws_bytes(cfg, plan_of(cfg, B, max_q, max_len, splits, 0), B, total_q);
     return KVQ_OK;
 }
 
@@ -515,7 +739,7 @@ int kvq_paged_attention(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, 
     if (q_stride < (int64_t)cfg->Hq * cfg->D) return KVQ_ERR_SHAPE;
     const Plan p = plan_of(cfg, B, max_q, max_len, splits, window);
     if ((int64_t)p.S * p.nrb > INT32_MAX) return KVQ_ERR_RANGE;
-    const size_t need = ws_bytes(cfg, p, total_q);
+    const size_t need = ws_bytes(cfg, p, B, total_q);
     if (need > 0) {
         if (!workspace) return KVQ_ERR_NULL;
         if (!aligned16(workspace)) return KVQ_ERR_ALIGN;
@@ -531,34 +755,35 @@ int kvq_paged_attention(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, 
     a.out = (uint16_t*)out;
     a.lse = lse;
     a.part = (float*)workspace;
-    a.pml = (float2*)(a.part + (size_t)p.S * total_q * cfg->Hq * cfg->D);
+    const size_t prow = p.nt ? (size_t)2 * p.S * 8 * p.nt : (size_t)p.S * total_q * cfg->Hq;
+    if (p.join) {
+        a.pml = (float2*)(a.part + prow * cfg->D);
+        if (p.nt) {
+            a.rec = (int4*)(a.pml + prow);
+            a.by_request = (int64_t)B * cfg->Hkv <= p.S;
+        }
+    }
     a.total_q = total_q, a.max_q = max_q, a.max_len = max_len, a.window = window, a.S = p.S;
     a.scale_log2 = (float)ldexp((double)sm_scale * 1.4426950408889634, cfg->k_exp);
     a.out_scale = ldexpf(1.0f, cfg->v_exp);
     const bool bf = cfg->dtype == KVQ_BF16;
-    cudaError_t ce;
     cudaStream_t st = (cudaStream_t)stream;
     if (p.nt == 0) {
         if ((e = run_chunk(a, p.nrb, B, st))) return e;
-    } else {
-    int smem, warps;
-    const AttnKernel kern = cfg->D == 64 ? (bf ? attn_kernel<64, true>(p.nt, &smem, &warps)
-                                               : attn_kernel<64, false>(p.nt, &smem, &warps))
-                                         : (bf ? attn_kernel<128, true>(p.nt, &smem, &warps)
-                                               : attn_kernel<128, false>(p.nt, &smem, &warps));
-    ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (ce) return record_cuda(ce);
-    kern<<<dim3((unsigned)(p.S * p.nrb), cfg->Hkv, B), warps * 32, smem, st>>>(a);
-    if ((ce = cudaGetLastError())) return record_cuda(ce);
-    }
-    if (p.S > 1) {
-        auto* mk = cfg->D == 64 ? (bf ? k_paged_merge<64, true> : k_paged_merge<64, false>)
-                                : (bf ? k_paged_merge<128, true> : k_paged_merge<128, false>);
-        const int64_t R = (int64_t)max_q * (cfg->Hq / cfg->Hkv);
-        mk<<<dim3((unsigned)((R + kMergeWarps - 1) / kMergeWarps), cfg->Hkv, B), kMergeWarps * 32, 0, st>>>(a);
+        if (p.join) {
+            auto* mk = cfg->D == 64 ? (bf ? k_paged_merge<64, true> : k_paged_merge<64, false>)
+                                    : (bf ? k_paged_merge<128, true> : k_paged_merge<128, false>);
+            const int64_t R = (int64_t)max_q * (cfg->Hq / cfg->Hkv);
+            mk<<<dim3((unsigned)((R + kMergeWarps - 1) / kMergeWarps), cfg->Hkv, B), kMergeWarps * 32, 0, st>>>(a);
+        }
         return record_cuda(cudaGetLastError());
     }
-    return KVQ_OK;
+    const int rows = max_q * (cfg->Hq / cfg->Hkv);
+    if (cfg->D == 64)
+        return p.nt == 1 ? (bf ? run_few<64, 1, true>(a, p, B, rows, st) : run_few<64, 1, false>(a, p, B, rows, st))
+                         : (bf ? run_few<64, 2, true>(a, p, B, rows, st) : run_few<64, 2, false>(a, p, B, rows, st));
+    return p.nt == 1 ? (bf ? run_few<128, 1, true>(a, p, B, rows, st) : run_few<128, 1, false>(a, p, B, rows, st))
+                     : (bf ? run_few<128, 2, true>(a, p, B, rows, st) : run_few<128, 2, false>(a, p, B, rows, st));
 }
 
 }  // extern "C"

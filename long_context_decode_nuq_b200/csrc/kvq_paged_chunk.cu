@@ -494,12 +494,14 @@ int launch(const AttnArgs& a, int nrb, int B, cudaStream_t st) {
     auto* kern = k_paged_chunk<D, BF>;
     constexpr int smem = Smem<D>::total;
     static_assert(smem <= 232448, "shared memory of a block");
+    static SmemOptIn opt;
+    if (int e = opt.set((const void*)kern, smem)) return e;
     // the register split needs the launch's 128 registers a thread
-    cudaFuncAttributes at;
-    cudaError_t ce = cudaFuncGetAttributes(&at, kern);
-    if (ce) return record_cuda(ce);
-    if (at.numRegs * 4 < 2 * kRegSoft + kRegDeq + kRegIssue) return KVQ_ERR_UNSUPPORTED;
-    if ((ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return record_cuda(ce);
+    static const int regs = [&] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs * 4 < 2 * kRegSoft + kRegDeq + kRegIssue) return KVQ_ERR_UNSUPPORTED;
     kern<<<dim3((unsigned)(a.S * nrb), a.c.Hkv, B), kThreads, smem, st>>>(a, nrb);
     return record_cuda(cudaGetLastError());
 }

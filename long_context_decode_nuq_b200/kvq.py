@@ -492,7 +492,7 @@ class PagedCache:
     and lengths belong to the requests and are shared by all layers)."""
 
     def __init__(self, cfg: PagedCfg, device="cuda", pool=None):
-        import torch
+        torch = _torch()
         self.cfg = cfg
         n = kvq_paged_layout(cfg)
         if pool is None:
@@ -502,6 +502,7 @@ class PagedCache:
         self.pool = pool
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
         self.device = pool.device
+        self.index = pool.get_device()
         self.dtype = torch.bfloat16 if cfg.dtype else torch.float16
         self.struct = PagedStruct(pool.data_ptr(), self.status.data_ptr())
         self.args = byref(cfg), byref(self.struct)
@@ -510,43 +511,55 @@ class PagedCache:
         return self.pool.numel()
 
 
-def _call(where, fn, device, stream, *args):
-    """fn(*args, stream) on `device`, by its number."""
+_i32 = _raw_stream = _current = None
+
+
+def _torch():
+    """torch, and the names that the calls below need every time (a call costs a few microseconds
+    of host time, as much as the smallest kernels take)."""
+    global _i32, _raw_stream, _current
     import torch
-    i = device.index
-    if device.type != "cuda":
-        raise ValueError(f"{where}: the tensors are on {device}")
-    if stream is None:
-        stream = torch.cuda.current_stream(i)
-    if torch.cuda.current_device() == i:
-        code = fn(*args, stream.cuda_stream)
+    if _i32 is None:
+        _raw_stream, _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        _i32 = torch.int32
+    return torch
+
+
+def _call(where, fn, i, stream, *args):
+    """fn(*args, stream) on the device of number i (-1: host memory)."""
+    if i < 0:
+        raise ValueError(f"{where}: the tensors are not on a CUDA device")
+    s = _raw_stream(i) if stream is None else stream.cuda_stream
+    if _current() == i:
+        code = fn(*args, s)
     else:
-        with torch.cuda.device(i):
-            code = fn(*args, stream.cuda_stream)
+        with _torch().cuda.device(i):
+            code = fn(*args, s)
     if code != KVQ_OK:
         raise KvqError(code, where)
 
 
-def _ints(where, device, **tensors):
-    import torch
-    for name, t in tensors.items():
-        if t.dtype != torch.int32 or not t.is_contiguous() or t.device != device:
-            raise ValueError(f"{where}: {name} is a contiguous int32 tensor on {device}")
+def _ints(where, i, *tensors):
+    for t in tensors:
+        if t.dtype is not _i32 or t.get_device() != i or not t.is_contiguous():
+            raise ValueError(f"{where}: {tuple(t.shape)} {t.dtype} on {t.device} is not a contiguous "
+                             "int32 tensor on the call's device")
 
 
-def _rows(where, name, t, shape, dtype, device):
+def _rows(where, name, t, shape, dtype, i):
     """A [n, heads, D] tensor whose rows may lie apart; its row stride."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
+    if t.dtype is not dtype or t.get_device() != i or t.shape != shape:
         raise ValueError(f"{where}: {name} is {tuple(t.shape)} {t.dtype} on {t.device}, not "
-                         f"{shape} {dtype} on {device}")
-    st = t.stride()
-    if (shape[2] > 1 and st[2] != 1) or (shape[1] > 1 and st[1] != shape[2]):
+                         f"{shape} {dtype} on the call's device")
+    n, heads, d = shape
+    row, head, one = t.stride()
+    if (one != 1 and d > 1) or (head != d and heads > 1):
         raise ValueError(f"{where}: {name}'s heads and channels are not contiguous")
-    return st[0] if shape[0] > 1 else shape[1] * shape[2]
+    return row if n > 1 else heads * d
 
 
 def kvq_paged_reset(cache: PagedCache, stream=None) -> None:
-    _call("kvq_paged_reset", load().kvq_paged_reset, cache.device, stream, cache.args[1])
+    _call("kvq_paged_reset", load().kvq_paged_reset, cache.index, stream, cache.args[1])
 
 
 def kvq_paged_get_status(cache: PagedCache, stream=None) -> int:
@@ -559,23 +572,22 @@ def kvq_paged_get_status(cache: PagedCache, stream=None) -> int:
 
 
 def _table(where, cache, table, B):
-    _ints(where, cache.device, block_table=table)
-    if tuple(table.shape) != (B, cache.cfg.max_pages):
+    _ints(where, cache.index, table)
+    if table.shape != (B, cache.cfg.max_pages):
         raise ValueError(f"{where}: block_table is {tuple(table.shape)}, not "
                          f"{(B, cache.cfg.max_pages)}")
 
 
 def kvq_page_plan(cache: PagedCache, lens, n_new, block_table, free_pages, n_free, cu_new, len_out,
                   n_free_out, slots, positions, stream=None) -> None:
-    w, B = "kvq_page_plan", lens.numel()
-    _ints(w, cache.device, lens=lens, n_new=n_new, free_pages=free_pages, n_free=n_free,
-          cu_new=cu_new, len_out=len_out, n_free_out=n_free_out, slots=slots, positions=positions)
+    w, B, cap = "kvq_page_plan", lens.numel(), slots.numel()
+    _ints(w, cache.index, lens, n_new, free_pages, n_free, cu_new, len_out, n_free_out, slots,
+          positions)
     _table(w, cache, block_table, B)
-    cap = slots.numel()
     if (n_new.numel() != B or cu_new.numel() != B + 1 or len_out.numel() != B
             or n_free.numel() != 1 or n_free_out.numel() != 1 or positions.numel() != cap):
         raise ValueError(f"{w}: sizes do not agree with {B} requests and {cap} tokens")
-    _call(w, load().kvq_page_plan, cache.device, stream, *cache.args, B, lens.data_ptr(),
+    _call(w, load().kvq_page_plan, cache.index, stream, *cache.args, B, lens.data_ptr(),
           n_new.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(), cap,
           cu_new.data_ptr(), len_out.data_ptr(), n_free_out.data_ptr(), slots.data_ptr(),
           positions.data_ptr())
@@ -584,30 +596,33 @@ def kvq_page_plan(cache: PagedCache, lens, n_new, block_table, free_pages, n_fre
 def kvq_page_release(cache: PagedCache, lens, done, block_table, free_pages, n_free,
                      stream=None) -> None:
     w, B = "kvq_page_release", lens.numel()
-    _ints(w, cache.device, lens=lens, done=done, free_pages=free_pages, n_free=n_free)
+    _ints(w, cache.index, lens, done, free_pages, n_free)
     _table(w, cache, block_table, B)
     if done.numel() != B or n_free.numel() != 1 or free_pages.numel() < cache.cfg.num_pages:
         raise ValueError(f"{w}: sizes do not agree with {B} requests and {cache.cfg.num_pages} pages")
-    _call(w, load().kvq_page_release, cache.device, stream, *cache.args, B, lens.data_ptr(),
+    _call(w, load().kvq_page_release, cache.index, stream, *cache.args, B, lens.data_ptr(),
           done.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), n_free.data_ptr())
 
 
 def kvq_paged_append(cache: PagedCache, k, v, slots, stream=None) -> None:
-    w, c, n = "kvq_paged_append", cache.cfg, slots.numel()
-    _ints(w, cache.device, slots=slots)
-    ks = _rows(w, "k", k, (n, c.Hkv, c.D), cache.dtype, cache.device)
-    vs = _rows(w, "v", v, (n, c.Hkv, c.D), cache.dtype, cache.device)
-    _call(w, load().kvq_paged_append, cache.device, stream, *cache.args, k.data_ptr(), ks,
-          v.data_ptr(), vs, slots.data_ptr(), n)
+    w, c, i = "kvq_paged_append", cache.cfg, cache.index
+    n = slots.numel()
+    _ints(w, i, slots)
+    shape = n, c.Hkv, c.D
+    ks, vs = _rows(w, "k", k, shape, cache.dtype, i), _rows(w, "v", v, shape, cache.dtype, i)
+    _call(w, load().kvq_paged_append, i, stream, *cache.args, k.data_ptr(), ks, v.data_ptr(), vs,
+          slots.data_ptr(), n)
 
 
 def kvq_paged_dequantize(cache: PagedCache, slots, khat, vhat, stream=None) -> None:
-    w, c, n = "kvq_paged_dequantize", cache.cfg, slots.numel()
-    _ints(w, cache.device, slots=slots)
-    for name, t in (("khat", khat), ("vhat", vhat)):
-        if _rows(w, name, t, (n, c.Hkv, c.D), cache.dtype, cache.device) != c.Hkv * c.D:
-            raise ValueError(f"{w}: {name} is not contiguous")
-    _call(w, load().kvq_paged_dequantize, cache.device, stream, *cache.args, slots.data_ptr(), n,
+    w, c, i = "kvq_paged_dequantize", cache.cfg, cache.index
+    n = slots.numel()
+    _ints(w, i, slots)
+    shape = n, c.Hkv, c.D
+    if (_rows(w, "khat", khat, shape, cache.dtype, i) != c.Hkv * c.D
+            or _rows(w, "vhat", vhat, shape, cache.dtype, i) != c.Hkv * c.D):
+        raise ValueError(f"{w}: an output is not contiguous")
+    _call(w, load().kvq_paged_dequantize, i, stream, *cache.args, slots.data_ptr(), n,
           khat.data_ptr(), vhat.data_ptr())
 
 
@@ -623,30 +638,31 @@ def kvq_paged_attention(cache: PagedCache, q, cu_q, lens, block_table, max_q: in
                         sm_scale: float, out, workspace=None, window: int = 0, lse=None,
                         splits: int = 0, stream=None) -> None:
     """cu_q: int32 [B + 1], or None for one query per request."""
-    w, c, dev, B, n = "kvq_paged_attention", cache.cfg, cache.device, lens.numel(), q.shape[0]
-    _ints(w, dev, lens=lens)
+    w, c, i = "kvq_paged_attention", cache.cfg, cache.index
+    B, n = lens.numel(), q.shape[0]
+    _ints(w, i, lens)
     _table(w, cache, block_table, B)
-    qs = _rows(w, "q", q, (n, c.Hq, c.D), cache.dtype, dev)
-    if _rows(w, "out", out, (n, c.Hq, c.D), cache.dtype, dev) != c.Hq * c.D:
+    shape = n, c.Hq, c.D
+    qs = _rows(w, "q", q, shape, cache.dtype, i)
+    if _rows(w, "out", out, shape, cache.dtype, i) != c.Hq * c.D:
         raise ValueError(f"{w}: out is not contiguous")
     cu = l = ws = None
     wb = 0
     if cu_q is not None:
-        _ints(w, dev, cu_q=cu_q)
+        _ints(w, i, cu_q)
         if cu_q.numel() != B + 1:
             raise ValueError(f"{w}: cu_q has {cu_q.numel()} entries for {B} requests")
         cu = cu_q.data_ptr()
     if lse is not None:
-        import torch
-        if (lse.dtype != torch.float32 or lse.device != dev or tuple(lse.shape) != (n, c.Hq)
+        if (lse.dtype is not _torch().float32 or lse.get_device() != i or lse.shape != shape[:2]
                 or not lse.is_contiguous()):
-            raise ValueError(f"{w}: lse is a contiguous float32 tensor {(n, c.Hq)} on {dev}")
+            raise ValueError(f"{w}: lse is a contiguous float32 tensor {shape[:2]} on q's device")
         l = lse.data_ptr()
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"{w}: the workspace is a contiguous tensor on {dev}")
+        if workspace.get_device() != i or not workspace.is_contiguous():
+            raise ValueError(f"{w}: the workspace is a contiguous tensor on q's device")
         ws, wb = workspace.data_ptr(), workspace.nbytes
-    _call(w, load().kvq_paged_attention, dev, stream, *cache.args, q.data_ptr(), qs, cu, B, n,
+    _call(w, load().kvq_paged_attention, i, stream, *cache.args, q.data_ptr(), qs, cu, B, n,
           lens.data_ptr(), block_table.data_ptr(), max_q, max_len, sm_scale, window,
           out.data_ptr(), l, ws, wb, splits)
 
@@ -665,22 +681,22 @@ def kvq_rope(cfg: RopeCfg, q, k, positions, freqs, q_out, k_out, inverse=False,
              stream=None) -> None:
     """q, k [n, heads, D] (k may be None when cfg.Hkv is 0), positions int32 [axes, n], freqs
     float64 [rot_dim / 2]; q_out and k_out may be q and k."""
-    import torch
-    w, n, dev = "kvq_rope", q.shape[0], q.device
+    torch = _torch()
+    w, n, i, Hkv, d = "kvq_rope", q.shape[0], q.get_device(), cfg.Hkv, cfg.D
     dtype = (torch.float16, torch.bfloat16, torch.float32)[cfg.dtype]
-    _ints(w, dev, positions=positions)
-    if tuple(positions.shape) != (cfg.axes, n) and not (cfg.axes == 1 and positions.numel() == n):
+    _ints(w, i, positions)
+    if positions.shape != (cfg.axes, n) and not (cfg.axes == 1 and positions.numel() == n):
         raise ValueError(f"{w}: positions is {tuple(positions.shape)}, not {(cfg.axes, n)}")
-    if (freqs.dtype != torch.float64 or freqs.numel() != cfg.rot_dim // 2 or freqs.device != dev
-            or not freqs.is_contiguous()):
-        raise ValueError(f"{w}: freqs is a float64 tensor of {cfg.rot_dim // 2} on {dev}")
-    qs = _rows(w, "q", q, (n, cfg.Hq, cfg.D), dtype, dev)
-    qos = _rows(w, "q_out", q_out, (n, cfg.Hq, cfg.D), dtype, dev)
+    if (freqs.dtype is not torch.float64 or freqs.numel() != cfg.rot_dim // 2
+            or freqs.get_device() != i or not freqs.is_contiguous()):
+        raise ValueError(f"{w}: freqs is a float64 tensor of {cfg.rot_dim // 2} on q's device")
+    shape = n, cfg.Hq, d
+    qs, qos = _rows(w, "q", q, shape, dtype, i), _rows(w, "q_out", q_out, shape, dtype, i)
     kp = kop = None
     ks = kos = 0
-    if cfg.Hkv:
-        ks = _rows(w, "k", k, (n, cfg.Hkv, cfg.D), dtype, dev)
-        kos = _rows(w, "k_out", k_out, (n, cfg.Hkv, cfg.D), dtype, dev)
+    if Hkv:
+        shape = n, Hkv, d
+        ks, kos = _rows(w, "k", k, shape, dtype, i), _rows(w, "k_out", k_out, shape, dtype, i)
         kp, kop = k.data_ptr(), k_out.data_ptr()
-    _call(w, load().kvq_rope, dev, stream, byref(cfg), q.data_ptr(), qs, kp, ks,
+    _call(w, load().kvq_rope, i, stream, byref(cfg), q.data_ptr(), qs, kp, ks,
           positions.data_ptr(), freqs.data_ptr(), n, int(inverse), q_out.data_ptr(), qos, kop, kos)

@@ -79,15 +79,20 @@ def test_release(change, code):
     ({11: float("nan")}, RANGE), ({11: float("inf")}, RANGE), ({12: -1}, RANGE), ({13: A + 2}, ALIGN), ({13: None}, NULL), ({15: None}, NULL),
     ({15: A + 8}, ALIGN), ({16: 10}, WORKSPACE), ({17: 257}, RANGE), ({17: -1}, RANGE)])
 def test_attention(change, code):
-    a = [ctypes.byref(cfg()), cache(), A, 1024, A, 3, 9, A, A, 4, 64, 0.1, 0, A, None, A, 1 << 30, 2, None]
+    a = [ctypes.byref(cfg()), cache(), A, 1024, A, 3, 9, A, A, 4, 640, 0.1, 0, A, None, A, 1 << 30, 2, None]
     for i, x in change.items():
         a[i] = x
     assert call("kvq_paged_attention", *a) == code
 
 
-def test_workspace_is_enough_for_any_window():
+def test_workspace_sizes():
+    # 16 rows a kv head: pieces of two per block, and a count per request
     n = [K.kvq_paged_attention_workspace(cfg(), 3, 9, 4, 5000, s) for s in (0, 1, 2, 256)]
-    assert n[1] == 0 < n[2] < n[3] and n[2] == 2 * 9 * 8 * 130 * 4
+    assert n[1] == 2 * 6 * 16 * 130 * 4 + 6 * 16 and n[1] < n[2] < n[0] < n[3]
+    # 800 rows: splits of all rows
+    n = [K.kvq_paged_attention_workspace(cfg(), 3, 600, 200, 5000, s) for s in (1, 2, 256)]
+    assert n == [0, 2 * 600 * 8 * 130 * 4, 256 * 600 * 8 * 130 * 4]
+    assert K.kvq_paged_attention_workspace(cfg(), 3, 3, 1, 64) == 0
 
 
 @pytest.mark.parametrize("kw,change,code", [
