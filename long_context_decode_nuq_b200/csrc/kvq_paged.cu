@@ -87,66 +87,107 @@ __device__ __forceinline__ int find_last(const uint32_t* v, int n, uint32_t x) {
     return lo;
 }
 
+// ITEMS requests a thread, consecutive ones.  A cluster of eight blocks at most: 8192 threads.
+template <int ITEMS>
 __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
-    __shared__ uint32_t s_tok[kPlanThreads], s_page[kPlanThreads];
-    __shared__ int32_t s_len[kPlanThreads];
-    __shared__ uint8_t s_ok[kPlanThreads];
+    extern __shared__ uint32_t s_plan[];  // per request of the chunk: first token, first page, length
     __shared__ long long s_scan[2][32];
     __shared__ int s_used;
-    const int tid = threadIdx.x, nt = blockDim.x;
+    constexpr int kAtOnce = 4;  // tokens a thread looks up together
+    const int tid = threadIdx.x, nt = blockDim.x, chunk = nt * ITEMS;
+    uint32_t *s_tok = s_plan, *s_page = s_plan + chunk, *s_len = s_plan + 2 * chunk;  // length: top bit, accepted
     const int rank = blockIdx.x, nc = gridDim.x;  // the grid is one cluster
+    const int lp = 31 - __clz(a.P), pm = a.P - 1;
     const int n_free = min(max(*a.n_free, 0), a.num_pages);
     long long tok0 = 0, page0 = 0;
     int bad = 0;
     if (tid == 0) s_used = 0;
-    for (int base = 0; base < a.B; base += nt) {
-        const int b = base + tid, m = min(nt, a.B - base);
-        const int len = b < a.B ? max(a.len[b], 0) : 0;
-        const int n = b < a.B ? max(a.n_new[b], 0) : 0;
-        const long long want = ((long long)len + n + a.P - 1) / a.P;
-        const long long have = ((long long)len + a.P - 1) / a.P;
-        const bool over = want > a.max_pages;
-        const long long need = over ? 0 : want - have;
-        long long t = n, p = need, tt, tp;
+    for (int base = 0; base < a.B; base += chunk) {
+        const int b0 = base + tid * ITEMS, m = min(chunk, a.B - base);
+        int len[ITEMS], n[ITEMS];
+        long long need[ITEMS], t = 0, p = 0, tt, tp;
+        bool over[ITEMS];
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            len[i] = b0 + i < a.B ? max(a.len[b0 + i], 0) : 0;
+            n[i] = b0 + i < a.B ? max(a.n_new[b0 + i], 0) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const long long want = ((long long)len[i] + n[i] + pm) >> lp, have = ((long long)len[i] + pm) >> lp;
+            over[i] = want > a.max_pages;
+            need[i] = over[i] ? 0 : want - have;
+            t += n[i];
+            p += need[i];
+        }
+        const long long tm = t, pmine = p;
         scan2(t, p, s_scan, &tt, &tp);
-        const long long tend = tok0 + t, pend = page0 + p;
-        const bool fits = need == 0 || pend <= n_free;
-        const bool ok = !over && tend <= a.capacity && fits;
-        s_tok[tid] = (uint32_t)min(t - n, (long long)a.capacity);
-        s_page[tid] = (uint32_t)min(p - need, (long long)a.num_pages);
-        s_len[tid] = len;
-        s_ok[tid] = ok;
-        if (b < a.B && ok && need > 0) atomicMax(&s_used, (int)pend);
-        if (b < a.B && !ok)
-            bad |= (over || tend > a.capacity) ? KVQ_STATUS_LEN_OVERFLOW : KVQ_STATUS_NO_PAGES;
+        long long tend = tok0 + t - tm, pend = page0 + p - pmine;
+        bool ok[ITEMS];
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            s_tok[tid * ITEMS + i] = (uint32_t)min(tend - tok0, (long long)a.capacity);
+            s_page[tid * ITEMS + i] = (uint32_t)min(pend - page0, (long long)a.num_pages);
+            tend += n[i];
+            pend += need[i];
+            ok[i] = !over[i] && tend <= a.capacity && (need[i] == 0 || pend <= n_free);
+            s_len[tid * ITEMS + i] = (uint32_t)len[i] | (ok[i] ? 0x80000000u : 0u);
+            if (b0 + i >= a.B) continue;
+            if (ok[i] && need[i] > 0) atomicMax(&s_used, (int)pend);
+            if (!ok[i]) bad |= (over[i] || tend > a.capacity) ? KVQ_STATUS_LEN_OVERFLOW : KVQ_STATUS_NO_PAGES;
+        }
         // every block has read this chunk's lengths before len_out, maybe the same buffer, changes
         if (nc > 1) cluster_sync(); else __syncthreads();
-        if (rank == 0 && b < a.B) {
-            a.cu[b] = (int32_t)min(tend - n, (long long)INT32_MAX);
-            a.len_out[b] = ok ? len + n : len;
+        if (rank == 0) {
+            long long c = tok0 + t - tm;
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i)
+                if (b0 + i < a.B) {
+                    a.cu[b0 + i] = (int32_t)min(c, (long long)INT32_MAX);
+                    a.len_out[b0 + i] = ok[i] ? len[i] + n[i] : len[i];
+                    c += n[i];
+                }
         }
-        const long long tlast = min(tok0 + tt, (long long)a.capacity);
-        for (long long i = tok0 + rank * nt + tid; i < tlast; i += (long long)nc * nt) {
-            const uint32_t rel = (uint32_t)(i - tok0);
-            const int j = find_last(s_tok, m, rel);
-            const long long pos = (long long)s_len[j] + (rel - s_tok[j]);
-            int slot = -1;
-            if (s_ok[j]) {
-                const int pi = (int)(pos / a.P), hv = (int)(((long long)s_len[j] + a.P - 1) / a.P);
-                const int page =
-                    pi < hv ? a.table[(size_t)(base + j) * a.max_pages + pi]
-                            : a.free_pages[n_free - 1 - (int)(page0 + s_page[j] + (pi - hv))];
-                if (page >= 0 && page < a.num_pages) slot = page * a.P + (int)(pos % a.P);
-                else bad |= KVQ_STATUS_BAD_PAGE;
+        const int ntok = (int)min(tt, max((long long)a.capacity - tok0, 0LL));
+        for (int i = rank * nt + tid; i < ntok; i += kAtOnce * nc * nt) {
+            int slot[kAtOnce], page[kAtOnce];
+            long long pos[kAtOnce];
+#pragma unroll
+            for (int z = 0; z < kAtOnce; ++z) {
+                const int rel = i + z * nc * nt;
+                slot[z] = page[z] = -1;
+                pos[z] = 0;
+                if (rel >= ntok) continue;
+                const int j = find_last(s_tok, m, (uint32_t)rel);
+                const uint32_t lj = s_len[j];
+                const int ln = (int)(lj & 0x7fffffffu);
+                pos[z] = (long long)ln + ((uint32_t)rel - s_tok[j]);
+                if (lj >> 31) {  // accepted, so the position fits
+                    const int pi = (int)(pos[z] >> lp), hv = (int)(((long long)ln + pm) >> lp);
+                    page[z] = pi < hv ? a.table[(size_t)(base + j) * a.max_pages + pi]
+                                      : a.free_pages[n_free - 1 - (int)(page0 + s_page[j] + (pi - hv))];
+                    slot[z] = 0;
+                }
             }
-            a.slots[i] = slot;
-            a.pos[i] = (int32_t)min(pos, (long long)INT32_MAX);
+#pragma unroll
+            for (int z = 0; z < kAtOnce; ++z) {
+                const int rel = i + z * nc * nt;
+                if (rel >= ntok) break;
+                if (slot[z] == 0) {
+                    const bool in = page[z] >= 0 && page[z] < a.num_pages;
+                    slot[z] = in ? (page[z] << lp) + (int)(pos[z] & pm) : -1;
+                    if (!in) bad |= KVQ_STATUS_BAD_PAGE;
+                }
+                a.slots[tok0 + rel] = slot[z];
+                a.pos[tok0 + rel] = (int32_t)min(pos[z], (long long)INT32_MAX);
+            }
         }
         const long long plast = min(tp, (long long)n_free - page0);
         for (long long r = rank * nt + tid; r < plast; r += (long long)nc * nt) {
             const int j = find_last(s_page, m, (uint32_t)r);
-            if (!s_ok[j]) continue;
-            const int hv = (int)(((long long)s_len[j] + a.P - 1) / a.P);
+            const uint32_t lj = s_len[j];
+            if (!(lj >> 31)) continue;
+            const int hv = (int)(((long long)(lj & 0x7fffffffu) + pm) >> lp);
             a.table[(size_t)(base + j) * a.max_pages + hv + (int)(r - s_page[j])] =
                 a.free_pages[n_free - 1 - (int)(page0 + r)];
         }
@@ -162,6 +203,29 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
         *a.n_free_out = n_free - s_used;
     }
     if (bad && (rank == 0 || (bad & KVQ_STATUS_BAD_PAGE))) atomicOr(a.status, bad);
+}
+
+template <int ITEMS>
+cudaError_t launch_plan(const PlanArgs& a, int blocks, int threads, cudaStream_t st) {
+    const size_t smem = (size_t)threads * ITEMS * 12;
+    static SmemOptIn opt;
+    if (ITEMS > 1 && opt.set((const void*)k_page_plan<ITEMS>, kPlanThreads * ITEMS * 12)) return cudaGetLastError();
+    if (blocks == 1) {
+        k_page_plan<ITEMS><<<1, threads, smem, st>>>(a);
+        return cudaGetLastError();
+    }
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(blocks);
+    lc.blockDim = dim3(threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = blocks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, k_page_plan<ITEMS>, (const PlanArgs)a);
 }
 
 // Release: the same walk over requests, one block; pages pushed in request order.
@@ -201,12 +265,46 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // ---------------------------------------------------------------------------------
-// Append.  A thread quantizes 8 channels (one 16-byte load, one 4-byte store); two neighbours
-// share a scale.  The maximum is taken on the 16-bit values (exact).  y / s is y * rn(1/s) with
-// one residual step, q + (y - q s) r, which lands on the same side of every decision point
-// t in {0.25, 0.75, ..., 5} as y / s does, and on t itself when y = t s (checked over every 11-bit
-// y and 4-bit s; without the step 60 of them miss).  HBM bound: 2 + 9/16 bytes a value.
+// Append and read-back.  A thread has 8 channels of a head (16 bytes outside, 4 inside the pool) and
+// walks over tokens with them, kAhead at a time so that their loads are in flight together; a
+// token's place in the pool costs a shift and a multiply, the rest of the address is found once.
+// Two neighbours share a scale.  HBM bound: 2 + 9/16 bytes a value.
 constexpr int kAppThreads = 256;
+constexpr int kAhead = 4;
+
+// Where a thread works: chunk r (8 channels) of the rows of tokens i0, i0 + step, ... < i1.
+struct Walk {
+    int r, i0, i1, step;
+    size_t at;  // bytes from a token's (page, row 0 of group 0) to its code word
+};
+template <int D>
+__device__ __forceinline__ Walk walk_of(const kvq_paged_cfg& c, int n, int tokens, bool val) {
+    constexpr int TH = D / 8;
+    const int per = c.Hkv * TH, wide = min(per, kAppThreads);
+    const int lanes = kAppThreads / wide;  // tokens side by side in a block
+    Walk w;
+    const int tok = threadIdx.x / wide;
+    w.r = blockIdx.x * wide + threadIdx.x % wide;
+    w.step = lanes;
+    w.i0 = blockIdx.y * tokens + tok;
+    w.i1 = tok < lanes && w.r < per ? min(n, (int)(blockIdx.y + 1) * tokens) : 0;
+    const int h = w.r / TH;
+    w.at = (size_t)h * (c.page_tokens / kGroup) * Paged<D>::kBytes + (val ? Paged<D>::kHalf : 0) + (w.r % TH) * 4;
+    return w;
+}
+// Bytes from the pool's start (kv head 0) to the row of a slot.
+template <int D>
+__device__ __forceinline__ size_t row_at(const kvq_paged_cfg& c, int slot, int lp) {
+    const int page = slot >> lp, t = slot & (c.page_tokens - 1);
+    return (size_t)page * ((size_t)c.Hkv * (c.page_tokens / kGroup) * Paged<D>::kBytes) + (t / kGroup) * Paged<D>::kBytes +
+           (t % kGroup) * Paged<D>::kRow;
+}
+// From a row's codes to its scale, for the word r % TH of the row.
+template <int D>
+__device__ __forceinline__ int scale_off(int slot, int r) {
+    const int t = slot % kGroup, c = r % (D / 8);
+    return (kGroup - t) * Paged<D>::kRow + t * Paged<D>::kScales + c / 2 - c * 4;
+}
 
 __device__ __forceinline__ bool slot_ok(int slot, int limit, int32_t* status) {
     if (slot < 0 || slot >= limit) {
@@ -216,124 +314,151 @@ __device__ __forceinline__ bool slot_ok(int slot, int limit, int32_t* status) {
     return true;
 }
 
+// Codes of 8 values and the scale byte of their 16.  The maximum is taken on the 16-bit values
+// (exact).  amax / 6 is amax * rn(1/6), and y / s is q = y r with r near 1/s and one residual step,
+// q + (y - q s) r: both land on the same side of every decision point as the quotients do, and on
+// the point itself when the quotient is one (checked over every 11-bit significand and every
+// scale; without the residual step 60 quotients miss).
+template <bool BF>
+__device__ __forceinline__ uint32_t quantize8(const uint4 w4, float down, float up, uint32_t pair, uint32_t* scale) {
+    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+    // |x| of a 16-bit float orders as its bits, NaNs above infinity
+    uint32_t mx = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+    mx = max(mx & 0xffffu, mx >> 16);
+    mx = max(mx, __shfl_xor_sync(pair, mx, 1));
+    float x[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[2 * q] = lo16<BF>(w[q]), x[2 * q + 1] = hi16<BF>(w[q]);
+    float am = lo16<BF>(mx);
+    if (mx >= (BF ? 0x7f80u : 0x7c00u)) {  // infinities or NaNs among the 16
+        am = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            if (x[q] != x[q]) x[q] = 0.0f;
+            am = fmaxf(am, fabsf(x[q]));
+            x[q] = fminf(fmaxf(x[q], -1e30f), 1e30f);
+        }
+        am = fmaxf(am, __shfl_xor_sync(pair, am, 1));
+    }
+    uint16_t sb;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sb) : "f"(0.0f), "f"(am * down * 0.16666667f));
+    const float s = __half2float(__ushort_as_half((uint16_t)e4m3x2(sb))) * up;
+    float rs;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(rs) : "f"(s));
+    if (s == 0.0f) rs = 0.0f;
+    uint32_t code = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float y[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const float y0 = x[2 * q + z] * rs;
+            y[z] = fmaf(fmaf(-y0, s, x[2 * q + z]), rs, y0);
+        }
+        uint16_t c2;
+        asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\t"
+            "cvt.u16.u8 %0, c;\n\t}"
+            : "=h"(c2)
+            : "f"(y[1]), "f"(y[0]));
+        code |= (uint32_t)c2 << (8 * q);
+    }
+    *scale = sb;
+    return code;
+}
+
 template <int D, bool BF>
 __global__ void __launch_bounds__(kAppThreads)
     k_paged_append(const kvq_paged_cfg cfg, uint8_t* pool, int32_t* status,
                    const uint16_t* __restrict__ k, int64_t ks, const uint16_t* __restrict__ v,
-                   int64_t vs, const int32_t* __restrict__ slots, int n) {
-    constexpr int TH = D / 8;  // threads of one token's head
-    const bool val = blockIdx.y;
-    const int per = cfg.Hkv * TH;
-    const int64_t total = (int64_t)n * per;
-    const uint16_t* src = val ? v : k;
+                   int64_t vs, const int32_t* __restrict__ slots, int n, int tokens) {
+    const bool val = blockIdx.z;
+    const Walk w = walk_of<D>(cfg, n, tokens, val);
+    const uint16_t* src = (val ? v : k) + w.r * 8;
     const int64_t stride = val ? vs : ks;
-    const int e = val ? cfg.v_exp : cfg.k_exp;
+    const int e = val ? cfg.v_exp : cfg.k_exp, lp = 31 - __clz(cfg.page_tokens), limit = cfg.num_pages << lp;
     const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
-    // total and the step are even, so a scale's two threads leave the loop together; the mask of
-    // the shuffle names the pair
+    // a scale's two threads have the same tokens; the mask of the shuffle names the pair
     const uint32_t pair = 3u << (threadIdx.x & 30);
-    for (int64_t it = (int64_t)blockIdx.x * kAppThreads + threadIdx.x; it < total;
-         it += (int64_t)gridDim.x * kAppThreads) {
-        const int i = (int)(it / per), r = (int)(it % per);
-        const uint4 w4 = __ldcs(reinterpret_cast<const uint4*>(src + i * stride + r * 8));
-        const int slot = slots[i];
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-        // largest |x| of 16 channels; |x| of a 16-bit float orders as its bits, NaNs above
-        // infinity
-        uint32_t mx = 0;
+    for (int i = w.i0; i < w.i1; i += kAhead * w.step) {
+        uint4 x[kAhead];
+        int slot[kAhead];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) mx = __vmaxu2(mx, w[q] & 0x7fff7fffu);
-        mx = max(mx & 0xffffu, mx >> 16);
-        mx = max(mx, __shfl_xor_sync(pair, mx, 1));
-        float x[8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) x[2 * q] = lo16<BF>(w[q]), x[2 * q + 1] = hi16<BF>(w[q]);
-        float am = lo16<BF>(mx);
-        if (mx >= (BF ? 0x7f80u : 0x7c00u)) {  // infinities or NaNs among the 16
-            am = 0.0f;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                if (x[q] != x[q]) x[q] = 0.0f;
-                am = fmaxf(am, fabsf(x[q]));
-                x[q] = fminf(fmaxf(x[q], -1e30f), 1e30f);
-            }
-            am = fmaxf(am, __shfl_xor_sync(pair, am, 1));
+        for (int z = 0; z < kAhead; ++z) {
+            const int j = i + z * w.step;
+            slot[z] = -1;
+            if (j < w.i1) slot[z] = slots[j], x[z] = __ldcs(reinterpret_cast<const uint4*>(src + j * stride));
         }
-        const float a6 = __fdiv_rn(am * down, 6.0f);
-        uint16_t sb;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sb) : "f"(0.0f), "f"(a6));
-        const float s = __half2float(__ushort_as_half((uint16_t)e4m3x2(sb))) * up;
-        const float rs = s > 0.0f ? __frcp_rn(s) : 0.0f;
-        uint32_t code = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float y[2];
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                const float y0 = x[2 * q + z] * rs;
-                y[z] = fmaf(fmaf(-y0, s, x[2 * q + z]), rs, y0);
-            }
-            uint16_t c2;
-            asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\t"
-                "cvt.u16.u8 %0, c;\n\t}"
-                : "=h"(c2)
-                : "f"(y[1]), "f"(y[0]));
-            code |= (uint32_t)c2 << (8 * q);
+        for (int z = 0; z < kAhead; ++z) {
+            if (!slot_ok(slot[z], limit, status)) continue;  // the same for both threads of a pair
+            uint32_t sb;
+            const uint32_t code = quantize8<BF>(x[z], down, up, pair, &sb);
+            uint8_t* g = pool + row_at<D>(cfg, slot[z], lp) + w.at;
+            *reinterpret_cast<uint32_t*>(g) = code;
+            if ((w.r & 1) == 0) g[scale_off<D>(slot[z], w.r)] = (uint8_t)sb;
         }
-        if (!slot_ok(slot, cfg.num_pages * cfg.page_tokens, status)) continue;
-        const int page = slot / cfg.page_tokens, t = slot % cfg.page_tokens;
-        const int h = r / TH, c = r % TH;
-        uint8_t* g = pool + group_at(cfg, page, h, t / kGroup) + (val ? Paged<D>::kHalf : 0);
-        *reinterpret_cast<uint32_t*>(g + (t % kGroup) * Paged<D>::kRow + c * 4) = code;
-        if ((c & 1) == 0)
-            g[kGroup * Paged<D>::kRow + (t % kGroup) * Paged<D>::kScales + c / 2] = (uint8_t)sb;
     }
 }
 
-// Read-back: the same split of work, the other way; HBM bound.
 template <int D, bool BF>
 __global__ void __launch_bounds__(kAppThreads)
     k_paged_dequant(const kvq_paged_cfg cfg, const uint8_t* __restrict__ pool, int32_t* status,
                     const int32_t* __restrict__ slots, int n, uint16_t* __restrict__ khat,
-                    uint16_t* __restrict__ vhat) {
-    constexpr int TH = D / 8;
-    const bool val = blockIdx.y;
-    const int per = cfg.Hkv * TH;
-    const int64_t total = (int64_t)n * per;
-    uint16_t* dst = val ? vhat : khat;
-    const int e = val ? cfg.v_exp : cfg.k_exp;
+                    uint16_t* __restrict__ vhat, int tokens) {
+    const bool val = blockIdx.z;
+    const Walk w = walk_of<D>(cfg, n, tokens, val);
+    uint16_t* dst = (val ? vhat : khat) + w.r * 8;
+    const int64_t stride = (int64_t)cfg.Hkv * D;
+    const int e = val ? cfg.v_exp : cfg.k_exp, lp = 31 - __clz(cfg.page_tokens), limit = cfg.num_pages << lp;
     const float up = __uint_as_float((uint32_t)(127 + e) << 23);
     const float top = BF ? 3.38953138925153547590e38f : 65504.0f;
-    for (int64_t it = (int64_t)blockIdx.x * kAppThreads + threadIdx.x; it < total;
-         it += (int64_t)gridDim.x * kAppThreads) {
-        const int i = (int)(it / per), r = (int)(it % per);
-        const int slot = slots[i];
-        uint4 o = make_uint4(0, 0, 0, 0);
-        if (slot_ok(slot, cfg.num_pages * cfg.page_tokens, status)) {
-            const int page = slot / cfg.page_tokens, t = slot % cfg.page_tokens;
-            const int h = r / TH, c = r % TH;
-            const uint8_t* g = pool + group_at(cfg, page, h, t / kGroup) + (val ? Paged<D>::kHalf : 0);
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(g + (t % kGroup) * Paged<D>::kRow + c * 4);
-            const uint32_t sb = g[kGroup * Paged<D>::kRow + (t % kGroup) * Paged<D>::kScales + c / 2];
-            const uint32_t s2 = e4m3x2(sb | sb << 8);
-            uint32_t h2[4], q[4];
-            e2m1x8(w, h2);
+    const bool plain = !BF && e == 0;  // the fp16 product is the value
+    for (int i = w.i0; i < w.i1; i += kAhead * w.step) {
+        uint32_t code[kAhead], sb[kAhead];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const uint32_t p = hmul2(h2[z], s2);
-                const float lo = fminf(fmaxf(lo16<false>(p) * up, -top), top);
-                const float hi = fminf(fmaxf(hi16<false>(p) * up, -top), top);
-                q[z] = pack16<BF>(lo, hi);
+        for (int z = 0; z < kAhead; ++z) {
+            const int j = i + z * w.step;
+            code[z] = sb[z] = 0;
+            if (j < w.i1) {
+                const int slot = slots[j];
+                if (slot_ok(slot, limit, status)) {
+                    const uint8_t* g = pool + row_at<D>(cfg, slot, lp) + w.at;
+                    code[z] = *reinterpret_cast<const uint32_t*>(g);
+                    sb[z] = g[scale_off<D>(slot, w.r)];
+                }
             }
-            o = make_uint4(q[0], q[1], q[2], q[3]);
         }
-        __stcs(reinterpret_cast<uint4*>(dst + it * 8), o);
+#pragma unroll
+        for (int z = 0; z < kAhead; ++z) {
+            const int j = i + z * w.step;
+            if (j >= w.i1) break;
+            const uint32_t s2 = e4m3x2(sb[z] | sb[z] << 8);
+            uint32_t h2[4];
+            e2m1x8(code[z], h2);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                h2[q] = hmul2(h2[q], s2);
+                if (!plain) {
+                    const float lo = fminf(fmaxf(lo16<false>(h2[q]) * up, -top), top);
+                    const float hi = fminf(fmaxf(hi16<false>(h2[q]) * up, -top), top);
+                    h2[q] = pack16<BF>(lo, hi);
+                }
+            }
+            __stcs(reinterpret_cast<uint4*>(dst + j * stride), make_uint4(h2[0], h2[1], h2[2], h2[3]));
+        }
     }
 }
 
-int app_blocks(int64_t items) {
-    const int64_t b = (items + kAppThreads - 1) / kAppThreads;
-    return (int)(b < 1 ? 1 : b > 148 * 64 ? 148 * 64 : b);
+// Blocks of both: across the chunks of a row, over runs of tokens (returned), keys and values.
+dim3 app_grid(const kvq_paged_cfg* c, int n, int* tokens) {
+    const int per = c->Hkv * c->D / 8, wide = per < kAppThreads ? per : kAppThreads;
+    const int lanes = kAppThreads / wide, across = (per + wide - 1) / wide;
+    // a token a thread while that leaves SMs idle, then up to four times kAhead; y stays in range
+    int64_t t = lanes;
+    while (t < 4 * kAhead * lanes && (int64_t)across * 2 * ((n + t - 1) / t) > 148 * 8) t *= 2;
+    while ((n + t - 1) / t > 65535) t *= 2;
+    *tokens = (int)t;
+    return dim3(across, (unsigned)((n + t - 1) / t), 2);
 }
 
 }  // namespace
@@ -379,21 +504,13 @@ int kvq_page_plan(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_
     if (B < 1 || B > (1 << 20) || capacity < 0) return KVQ_ERR_SHAPE;
     PlanArgs a{len,    n_new, free_pages, n_free, block_table,      cu_new,         len_out,        n_free_out, slots,
                positions, cache->status, B, cfg->page_tokens, cfg->num_pages, cfg->max_pages, capacity};
-    // one thread a request or token, in one block up to 8192 tokens: a cluster's start and its
-    // barriers cost about a microsecond
+    // a thread a request or token; one block up to 4096 tokens, since a cluster's start and its
+    // barriers cost about a microsecond; four requests a thread where there are more than threads
     const int most = B > capacity ? B : capacity;
     const int threads = most >= kPlanThreads ? kPlanThreads : (most + 31) / 32 * 32;
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(capacity > 8192 ? 8 : 1);
-    lc.blockDim = dim3(threads);
-    lc.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = lc.gridDim.x;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    lc.attrs = at;
-    lc.numAttrs = 1;
-    return record_cuda(cudaLaunchKernelEx(&lc, k_page_plan, (const PlanArgs)a));
+    const int blocks = capacity > 4096 ? 8 : 1;
+    cudaStream_t st = (cudaStream_t)stream;
+    return record_cuda(B > threads ? launch_plan<4>(a, blocks, threads, st) : launch_plan<1>(a, blocks, threads, st));
 }
 
 int kvq_page_release(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_t B,
@@ -425,9 +542,11 @@ int kvq_paged_append(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, con
     const bool bf = cfg->dtype == KVQ_BF16;
     auto* kern = cfg->D == 64 ? (bf ? k_paged_append<64, true> : k_paged_append<64, false>)
                               : (bf ? k_paged_append<128, true> : k_paged_append<128, false>);
-    kern<<<dim3(app_blocks(n * (row / 8)), 2), kAppThreads, 0, (cudaStream_t)stream>>>(
+    int tokens;
+    const dim3 grid = app_grid(cfg, n, &tokens);
+    kern<<<grid, kAppThreads, 0, (cudaStream_t)stream>>>(
         *cfg, cache->pool, cache->status, (const uint16_t*)k, k_stride, (const uint16_t*)v,
-        v_stride, slots, n);
+        v_stride, slots, n, tokens);
     return record_cuda(cudaGetLastError());
 }
 
@@ -443,9 +562,10 @@ int kvq_paged_dequantize(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache,
     const bool bf = cfg->dtype == KVQ_BF16;
     auto* kern = cfg->D == 64 ? (bf ? k_paged_dequant<64, true> : k_paged_dequant<64, false>)
                               : (bf ? k_paged_dequant<128, true> : k_paged_dequant<128, false>);
-    kern<<<dim3(app_blocks((int64_t)n * cfg->Hkv * cfg->D / 8), 2), kAppThreads, 0,
-           (cudaStream_t)stream>>>(*cfg, cache->pool, cache->status, slots, n, (uint16_t*)khat,
-                                   (uint16_t*)vhat);
+    int tokens;
+    const dim3 grid = app_grid(cfg, n, &tokens);
+    kern<<<grid, kAppThreads, 0, (cudaStream_t)stream>>>(
+        *cfg, cache->pool, cache->status, slots, n, (uint16_t*)khat, (uint16_t*)vhat, tokens);
     return record_cuda(cudaGetLastError());
 }
 

@@ -1,6 +1,8 @@
 // Layout and checks of the paged 4-bit cache (shared by its kernels).
 #pragma once
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 
 #include "kvq_device.cuh"
@@ -83,6 +85,21 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 }  // namespace kvq
 
 namespace kvq_host {
+// A kernel's leave to use more shared memory than the default, asked for once per device.
+struct SmemOptIn {
+    std::atomic<uint64_t> done{0};
+    int set(const void* kernel, int bytes) {
+        int dev = 0;
+        cudaError_t ce = cudaGetDevice(&dev);
+        if (ce) return record_cuda(ce);
+        const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+        if (done.load(std::memory_order_relaxed) & bit) return KVQ_OK;
+        ce = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (ce) return record_cuda(ce);
+        done.fetch_or(bit, std::memory_order_relaxed);
+        return KVQ_OK;
+    }
+};
 int check_paged_cfg(const kvq_paged_cfg* cfg);
 int check_paged_cache(const kvq_paged_cache* cache);
 }  // namespace kvq_host

@@ -1,8 +1,6 @@
 // What the two attention kernels over the paged cache share.
 #pragma once
 
-#include <atomic>
-
 #include "kvq_paged.cuh"
 
 namespace kvq {
@@ -50,21 +48,6 @@ __device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, f
 }  // namespace kvq
 
 namespace kvq_host {
-// A kernel's leave to use more shared memory than the default, asked for once per device.
-struct SmemOptIn {
-    std::atomic<uint64_t> done{0};
-    int set(const void* kernel, int bytes) {
-        int dev = 0;
-        cudaError_t ce = cudaGetDevice(&dev);
-        if (ce) return record_cuda(ce);
-        const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-        if (done.load(std::memory_order_relaxed) & bit) return KVQ_OK;
-        ce = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (ce) return record_cuda(ce);
-        done.fetch_or(bit, std::memory_order_relaxed);
-        return KVQ_OK;
-    }
-};
 // Prompt chunks (kvq_paged_chunk.cu): query rows of a block, and the launch.
 constexpr int kChunkRows = 256;
 int run_chunk(const kvq::AttnArgs& a, int nrb, int B, cudaStream_t stream);
