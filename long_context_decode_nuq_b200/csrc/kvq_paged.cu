@@ -265,21 +265,21 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // ---------------------------------------------------------------------------------
-// Append and read-back.  A thread has 8 channels of a head (16 bytes outside, 4 inside the pool) and
-// walks over tokens with them, kAhead at a time so that their loads are in flight together; a
-// token's place in the pool costs a shift and a multiply, the rest of the address is found once.
-// Two neighbours share a scale.  HBM bound: 2 + 9/16 bytes a value.
+// Append and read-back.  A thread has CH channels of a head -- 16, a scale's, to append; 8, a 16-byte
+// store, to read back -- and walks over tokens with them, kAhead at a time so that their loads are
+// in flight together; a token's place in the pool costs a shift and a multiply, the rest of the
+// address is found once.  HBM bound: 2 + 9/16 bytes a value.
 constexpr int kAppThreads = 256;
 constexpr int kAhead = 4;
 
-// Where a thread works: chunk r (8 channels) of the rows of tokens i0, i0 + step, ... < i1.
+// Where a thread works: chunk r (CH channels) of the rows of tokens i0, i0 + step, ... < i1.
 struct Walk {
     int r, i0, i1, step;
     size_t at;  // bytes from a token's (page, row 0 of group 0) to its code word
 };
-template <int D>
+template <int D, int CH>
 __device__ __forceinline__ Walk walk_of(const kvq_paged_cfg& c, int n, int tokens, bool val) {
-    constexpr int TH = D / 8;
+    constexpr int TH = D / CH;
     const int per = c.Hkv * TH, wide = min(per, kAppThreads);
     const int lanes = kAppThreads / wide;  // tokens side by side in a block
     Walk w;
@@ -289,7 +289,7 @@ __device__ __forceinline__ Walk walk_of(const kvq_paged_cfg& c, int n, int token
     w.i0 = blockIdx.y * tokens + tok;
     w.i1 = tok < lanes && w.r < per ? min(n, (int)(blockIdx.y + 1) * tokens) : 0;
     const int h = w.r / TH;
-    w.at = (size_t)h * (c.page_tokens / kGroup) * Paged<D>::kBytes + (val ? Paged<D>::kHalf : 0) + (w.r % TH) * 4;
+    w.at = (size_t)h * (c.page_tokens / kGroup) * Paged<D>::kBytes + (val ? Paged<D>::kHalf : 0) + (w.r % TH) * (CH / 2);
     return w;
 }
 // Bytes from the pool's start (kv head 0) to the row of a slot.
@@ -299,11 +299,11 @@ __device__ __forceinline__ size_t row_at(const kvq_paged_cfg& c, int slot, int l
     return (size_t)page * ((size_t)c.Hkv * (c.page_tokens / kGroup) * Paged<D>::kBytes) + (t / kGroup) * Paged<D>::kBytes +
            (t % kGroup) * Paged<D>::kRow;
 }
-// From a row's codes to its scale, for the word r % TH of the row.
-template <int D>
+// From the codes of chunk r to their scale.
+template <int D, int CH>
 __device__ __forceinline__ int scale_off(int slot, int r) {
-    const int t = slot % kGroup, c = r % (D / 8);
-    return (kGroup - t) * Paged<D>::kRow + t * Paged<D>::kScales + c / 2 - c * 4;
+    const int t = slot % kGroup, c = r % (D / CH);
+    return (kGroup - t) * Paged<D>::kRow + t * Paged<D>::kScales + c * CH / kGroup - c * (CH / 2);
 }
 
 __device__ __forceinline__ bool slot_ok(int slot, int limit, int32_t* status) {
@@ -314,31 +314,31 @@ __device__ __forceinline__ bool slot_ok(int slot, int limit, int32_t* status) {
     return true;
 }
 
-// Codes of 8 values and the scale byte of their 16.  The maximum is taken on the 16-bit values
-// (exact).  amax / 6 is amax * rn(1/6), and y / s is q = y r with r near 1/s and one residual step,
+// Codes of 16 values and their scale byte.  The maximum is taken on the 16-bit values (exact).
+// amax / 6 is amax * rn(1/6), and y / s is q = y r with r near 1/s and one residual step,
 // q + (y - q s) r: both land on the same side of every decision point as the quotients do, and on
 // the point itself when the quotient is one (checked over every 11-bit significand and every
 // scale; without the residual step 60 quotients miss).
 template <bool BF>
-__device__ __forceinline__ uint32_t quantize8(const uint4 w4, float down, float up, uint32_t pair, uint32_t* scale) {
-    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+__device__ __forceinline__ uint2 quantize16(const uint4 (&w4)[2], float down, float up, uint32_t* scale) {
+    const uint32_t w[8] = {w4[0].x, w4[0].y, w4[0].z, w4[0].w, w4[1].x, w4[1].y, w4[1].z, w4[1].w};
     // |x| of a 16-bit float orders as its bits, NaNs above infinity
-    uint32_t mx = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-    mx = max(mx & 0xffffu, mx >> 16);
-    mx = max(mx, __shfl_xor_sync(pair, mx, 1));
-    float x[8];
+    uint32_t mx = 0;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) x[2 * q] = lo16<BF>(w[q]), x[2 * q + 1] = hi16<BF>(w[q]);
+    for (int q = 0; q < 8; ++q) mx = __vmaxu2(mx, w[q] & 0x7fff7fffu);
+    mx = max(mx & 0xffffu, mx >> 16);
+    float x[16];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[2 * q] = lo16<BF>(w[q]), x[2 * q + 1] = hi16<BF>(w[q]);
     float am = lo16<BF>(mx);
-    if (mx >= (BF ? 0x7f80u : 0x7c00u)) {  // infinities or NaNs among the 16
+    if (mx >= (BF ? 0x7f80u : 0x7c00u)) {  // infinities or NaNs among them
         am = 0.0f;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
+        for (int q = 0; q < 16; ++q) {
             if (x[q] != x[q]) x[q] = 0.0f;
             am = fmaxf(am, fabsf(x[q]));
             x[q] = fminf(fmaxf(x[q], -1e30f), 1e30f);
         }
-        am = fmaxf(am, __shfl_xor_sync(pair, am, 1));
     }
     uint16_t sb;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sb) : "f"(0.0f), "f"(am * down * 0.16666667f));
@@ -346,24 +346,27 @@ __device__ __forceinline__ uint32_t quantize8(const uint4 w4, float down, float 
     float rs;
     asm("rcp.approx.f32 %0, %1;" : "=f"(rs) : "f"(s));
     if (s == 0.0f) rs = 0.0f;
-    uint32_t code = 0;
+    const unsigned long long r2 = pk(rs, rs), ns2 = pk(-s, -s);
+    uint32_t code[2];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        float y[2];
+    for (int h = 0; h < 2; ++h) {
+        f2 y[4];
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            const float y0 = x[2 * q + z] * rs;
-            y[z] = fmaf(fmaf(-y0, s, x[2 * q + z]), rs, y0);
+        for (int q = 0; q < 4; ++q) {
+            const unsigned long long v = pk(x[8 * h + 2 * q], x[8 * h + 2 * q + 1]), y0 = mul2(v, r2);
+            y[q] = upk(fma2(fma2(y0, ns2, v), r2, y0));
         }
-        uint16_t c2;
-        asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\t"
-            "cvt.u16.u8 %0, c;\n\t}"
-            : "=h"(c2)
-            : "f"(y[1]), "f"(y[0]));
-        code |= (uint32_t)c2 << (8 * q);
+        asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+            "mov.b32 %0, {a, b, c, d};\n\t}"
+            : "=r"(code[h])
+            : "f"(y[0].x), "f"(y[0].y), "f"(y[1].x), "f"(y[1].y), "f"(y[2].x), "f"(y[2].y), "f"(y[3].x), "f"(y[3].y));
     }
     *scale = sb;
-    return code;
+    return make_uint2(code[0], code[1]);
 }
 
 template <int D, bool BF>
@@ -372,30 +375,31 @@ __global__ void __launch_bounds__(kAppThreads)
                    const uint16_t* __restrict__ k, int64_t ks, const uint16_t* __restrict__ v,
                    int64_t vs, const int32_t* __restrict__ slots, int n, int tokens) {
     const bool val = blockIdx.z;
-    const Walk w = walk_of<D>(cfg, n, tokens, val);
-    const uint16_t* src = (val ? v : k) + w.r * 8;
+    const Walk w = walk_of<D, 16>(cfg, n, tokens, val);
+    const uint16_t* src = (val ? v : k) + w.r * 16;
     const int64_t stride = val ? vs : ks;
     const int e = val ? cfg.v_exp : cfg.k_exp, lp = 31 - __clz(cfg.page_tokens), limit = cfg.num_pages << lp;
     const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
-    // a scale's two threads have the same tokens; the mask of the shuffle names the pair
-    const uint32_t pair = 3u << (threadIdx.x & 30);
     for (int i = w.i0; i < w.i1; i += kAhead * w.step) {
-        uint4 x[kAhead];
+        uint4 x[kAhead][2];
         int slot[kAhead];
 #pragma unroll
         for (int z = 0; z < kAhead; ++z) {
             const int j = i + z * w.step;
             slot[z] = -1;
-            if (j < w.i1) slot[z] = slots[j], x[z] = __ldcs(reinterpret_cast<const uint4*>(src + j * stride));
+            if (j < w.i1) {
+                const uint4* p = reinterpret_cast<const uint4*>(src + j * stride);
+                slot[z] = slots[j], x[z][0] = p[0], x[z][1] = p[1];
+            }
         }
 #pragma unroll
         for (int z = 0; z < kAhead; ++z) {
-            if (!slot_ok(slot[z], limit, status)) continue;  // the same for both threads of a pair
+            if (!slot_ok(slot[z], limit, status)) continue;
             uint32_t sb;
-            const uint32_t code = quantize8<BF>(x[z], down, up, pair, &sb);
+            const uint2 code = quantize16<BF>(x[z], down, up, &sb);
             uint8_t* g = pool + row_at<D>(cfg, slot[z], lp) + w.at;
-            *reinterpret_cast<uint32_t*>(g) = code;
-            if ((w.r & 1) == 0) g[scale_off<D>(slot[z], w.r)] = (uint8_t)sb;
+            *reinterpret_cast<uint2*>(g) = code;
+            g[scale_off<D, 16>(slot[z], w.r)] = (uint8_t)sb;
         }
     }
 }
@@ -406,7 +410,7 @@ __global__ void __launch_bounds__(kAppThreads)
                     const int32_t* __restrict__ slots, int n, uint16_t* __restrict__ khat,
                     uint16_t* __restrict__ vhat, int tokens) {
     const bool val = blockIdx.z;
-    const Walk w = walk_of<D>(cfg, n, tokens, val);
+    const Walk w = walk_of<D, 8>(cfg, n, tokens, val);
     uint16_t* dst = (val ? vhat : khat) + w.r * 8;
     const int64_t stride = (int64_t)cfg.Hkv * D;
     const int e = val ? cfg.v_exp : cfg.k_exp, lp = 31 - __clz(cfg.page_tokens), limit = cfg.num_pages << lp;
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(kAppThreads)
                 if (slot_ok(slot, limit, status)) {
                     const uint8_t* g = pool + row_at<D>(cfg, slot, lp) + w.at;
                     code[z] = *reinterpret_cast<const uint32_t*>(g);
-                    sb[z] = g[scale_off<D>(slot, w.r)];
+                    sb[z] = g[scale_off<D, 8>(slot, w.r)];
                 }
             }
         }
@@ -450,8 +454,8 @@ __global__ void __launch_bounds__(kAppThreads)
 }
 
 // Blocks of both: across the chunks of a row, over runs of tokens (returned), keys and values.
-dim3 app_grid(const kvq_paged_cfg* c, int n, int* tokens) {
-    const int per = c->Hkv * c->D / 8, wide = per < kAppThreads ? per : kAppThreads;
+dim3 app_grid(const kvq_paged_cfg* c, int channels, int n, int* tokens) {
+    const int per = c->Hkv * c->D / channels, wide = per < kAppThreads ? per : kAppThreads;
     const int lanes = kAppThreads / wide, across = (per + wide - 1) / wide;
     // a token a thread while that leaves SMs idle, then up to four times kAhead; y stays in range
     int64_t t = lanes;
@@ -543,7 +547,7 @@ int kvq_paged_append(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, con
     auto* kern = cfg->D == 64 ? (bf ? k_paged_append<64, true> : k_paged_append<64, false>)
                               : (bf ? k_paged_append<128, true> : k_paged_append<128, false>);
     int tokens;
-    const dim3 grid = app_grid(cfg, n, &tokens);
+    const dim3 grid = app_grid(cfg, 16, n, &tokens);
     kern<<<grid, kAppThreads, 0, (cudaStream_t)stream>>>(
         *cfg, cache->pool, cache->status, (const uint16_t*)k, k_stride, (const uint16_t*)v,
         v_stride, slots, n, tokens);
@@ -563,7 +567,7 @@ int kvq_paged_dequantize(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache,
     auto* kern = cfg->D == 64 ? (bf ? k_paged_dequant<64, true> : k_paged_dequant<64, false>)
                               : (bf ? k_paged_dequant<128, true> : k_paged_dequant<128, false>);
     int tokens;
-    const dim3 grid = app_grid(cfg, n, &tokens);
+    const dim3 grid = app_grid(cfg, 8, n, &tokens);
     kern<<<grid, kAppThreads, 0, (cudaStream_t)stream>>>(
         *cfg, cache->pool, cache->status, slots, n, (uint16_t*)khat, (uint16_t*)vhat, tokens);
     return record_cuda(cudaGetLastError());
