@@ -50,18 +50,19 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 
 template <int NT>
-struct Shape {
-    static constexpr int W = NT == 1 ? 7 : 5;   // warps that compute (8 and 6 with the loader)
-    static constexpr int ST = NT == 1 ? 2 : 3;  // stages
-    static constexpr int threads = W * 32 + 32;
-};
+constexpr int kWarps = NT == 1 ? 7 : 5;        // that compute; one more loads
+template <int NT>
+constexpr int kStages = 3;
+template <int NT>
+constexpr int kFewThreads = kWarps<NT> * 32 + 32;
 template <int D, int NT>
 struct FewSmem {
-    static constexpr int W = Shape<NT>::W, ST = Shape<NT>::ST, RB = 8 * NT;
+    static constexpr int W = kWarps<NT>, ST = kStages<NT>, RB = 8 * NT;
     static constexpr int stage = W * 2 * Paged<D>::kBytes;
-    static constexpr int joint = ST * stage;                  // float [W][RB][D + 4]
-    static constexpr int ml = joint + W * RB * (D + 4) * 4;   // float2 [W][RB]
-    static constexpr int bar = ml + W * RB * 8;               // full[ST], empty[ST]
+    static constexpr int q = ST * stage;                      // uint2 [NT][D/16][32], then float [RB]
+    static constexpr int joint = q + NT * (D / 16) * 256 + RB * 4;  // float [W][4][D + 4]
+    static constexpr int ml = joint + W * 4 * (D + 4) * 4;    // float2 [W][4]
+    static constexpr int bar = ml + W * 4 * 8;                // full[ST], empty[ST]
     static constexpr int misc = bar + 16 * ST;                // got[ST], dead, start
     static constexpr int scan = misc + 64;                    // int64 [32]
     static constexpr int total = scan + 32 * 8;
@@ -106,7 +107,7 @@ __device__ __forceinline__ bool wait_or(uint64_t* bar, uint32_t parity, volatile
 }
 
 template <int D, int NT, bool BF>
-__global__ void __launch_bounds__(Shape<NT>::threads, 2) k_paged_attn(const AttnArgs a, int B) {
+__global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArgs a, int B) {
     using L = FewSmem<D, NT>;
     constexpr int W = L::W, ST = L::ST, RB = L::RB;
     constexpr int GB = Paged<D>::kBytes, HALF = Paged<D>::kHalf, ROW = Paged<D>::kRow, SC = Paged<D>::kScales;
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(Shape<NT>::threads, 2) k_paged_attn(const Attn
         base = __shfl_sync(0xffffffffu, incl - u, b) * Hkv;
         __syncthreads();
     } else {  // a thread a run of requests
-        const int per = (B + Shape<NT>::threads - 1) / Shape<NT>::threads;
+        const int per = (B + kFewThreads<NT> - 1) / kFewThreads<NT>;
         const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
         int64_t mine = 0;
         for (int r = b0; r < b1; ++r) {
@@ -251,18 +252,17 @@ __global__ void __launch_bounds__(Shape<NT>::threads, 2) k_paged_attn(const Attn
 
     const int tau = (g & 1) ? 4 + ((g >> 1) ^ 1) : (g >> 1);
     const int tv[4] = {t, 4 + (t ^ 1), 8 + t, 12 + (t ^ 1)};
+    uint2* s_q = reinterpret_cast<uint2*>(smem + L::q);
+    float* s_sl2 = reinterpret_cast<float*>(s_q + NT * KS * 32);
     float* so = reinterpret_cast<float*>(smem + L::joint);
     float2* sml = reinterpret_cast<float2*>(smem + L::ml);
     int k = 0;
     for (int64_t at = g0; at < g1; at += un) {
         piece(at);
         const Rows& rw = sg.rw;
-        // queries: lane (g, t) holds channels [t*D/4, (t+1)*D/4) of row g, as the columns of B
-        uint32_t qf[NT][KS][2];
-        float sl2[NT][2];
-        int pos[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        // queries, as the columns of B: lane (g, t) has channels [t*D/4, (t+1)*D/4) of row g.  They
+        // wait in shared memory, where a step's 8 bytes a lane cost less than the registers would.
+        for (int nt = warp; nt < NT; nt += W) {
             const int r = nt * 8 + g;
             uint32_t w[KS * 2] = {};
             if (r < rw.R) {
@@ -292,14 +292,19 @@ __global__ void __launch_bounds__(Shape<NT>::threads, 2) k_paged_attn(const Attn
                 for (int i = 0; i < KS * 2; ++i) w[i] = pack_h2(lo16<true>(w[i]) * f, hi16<true>(w[i]) * f);
             }
 #pragma unroll
-            for (int j = 0; j < KS; ++j) qf[nt][j][0] = w[2 * j], qf[nt][j][1] = w[2 * j + 1];
+            for (int j = 0; j < KS; ++j) s_q[(nt * KS + j) * 32 + lane] = make_uint2(w[2 * j], w[2 * j + 1]);
+            if (t == 0) s_sl2[nt * 8 + g] = fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + e) << 23), 1e-37f);
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
+        float sl2[NT][2];
+        int pos[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
-                const int er = __shfl_sync(0xffffffffu, e, (2 * t + z) * 4);
-                sl2[nt][z] = fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + er) << 23), 1e-37f);
+                sl2[nt][z] = s_sl2[nt * 8 + 2 * t + z];
                 pos[nt][z] = sg.first + (nt * 8 + 2 * t + z) / G;
             }
-        }
 
         float o[NT][KS][4] = {}, m[NT][2], l[NT][2] = {};
 #pragma unroll
@@ -317,45 +322,52 @@ __global__ void __launch_bounds__(Shape<NT>::threads, 2) k_paged_attn(const Attn
             const bool mask = got != 3u || t0 + 32 > sg.all_hi || t0 < sg.all_lo;
 
             float sc[2][NT][4];
+            uint32_t kc[2][2][KW], ks[2][2][2];  // codes and scale pairs (s, s) of the lane's channels
 #pragma unroll
             for (int gr = 0; gr < 2; ++gr) {
                 const uint8_t* kb = buf + gr * GB;
-                uint32_t kc[2][KW];
-                uint32_t ks[2][2];  // scale pairs (s, s) of the lane's channels
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                     const uint8_t* row = kb + (tau + 8 * z) * ROW + t * (D / 8);
                     const uint8_t* srow = kb + kGroup * ROW + (tau + 8 * z) * SC;
                     if constexpr (D == 128) {
                         const uint4 x = *reinterpret_cast<const uint4*>(row);
-                        kc[z][0] = x.x, kc[z][1] = x.y, kc[z][2] = x.z, kc[z][3] = x.w;
+                        kc[gr][z][0] = x.x, kc[gr][z][1] = x.y, kc[gr][z][2] = x.z, kc[gr][z][3] = x.w;
                         const uint32_t two = e4m3x2(*reinterpret_cast<const uint16_t*>(srow + 2 * t));
-                        ks[z][0] = __byte_perm(two, 0, 0x1010);
-                        ks[z][1] = __byte_perm(two, 0, 0x3232);
+                        ks[gr][z][0] = __byte_perm(two, 0, 0x1010);
+                        ks[gr][z][1] = __byte_perm(two, 0, 0x3232);
                     } else {
                         const uint2 x = *reinterpret_cast<const uint2*>(row);
-                        kc[z][0] = x.x, kc[z][1] = x.y;
+                        kc[gr][z][0] = x.x, kc[gr][z][1] = x.y;
                         const uint32_t one = srow[t];
-                        ks[z][0] = ks[z][1] = e4m3x2(one | one << 8);
+                        ks[gr][z][0] = ks[gr][z][1] = e4m3x2(one | one << 8);
                     }
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int z = 0; z < 4; ++z) sc[gr][nt][z] = 0.0f;
+            }
 #pragma unroll
-                for (int w = 0; w < KW; ++w) {
-                    uint32_t x0[4], x1[4];
-                    e2m1x8(kc[0][w], x0);
-                    e2m1x8(kc[1][w], x1);
+            for (int w = 0; w < KW; ++w) {
+                uint32_t x[2][2][4];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t s0 = ks[0][w * 2 / KW], s1 = ks[1][w * 2 / KW];
-                        const uint32_t A[4] = {hmul2(x0[2 * u], s0), hmul2(x1[2 * u], s1),
-                                               hmul2(x0[2 * u + 1], s0), hmul2(x1[2 * u + 1], s1)};
+                for (int gr = 0; gr < 2; ++gr) {
+                    e2m1x8(kc[gr][0][w], x[gr][0]);
+                    e2m1x8(kc[gr][1][w], x[gr][1]);
+                }
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816(sc[gr][nt], A, qf[nt][2 * w + u][0], qf[nt][2 * w + u][1]);
+                for (int u = 0; u < 2; ++u) {
+                    uint2 qf[NT];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) qf[nt] = s_q[(nt * KS + 2 * w + u) * 32 + lane];
+#pragma unroll
+                    for (int gr = 0; gr < 2; ++gr) {
+                        const uint32_t s0 = ks[gr][0][w * 2 / KW], s1 = ks[gr][1][w * 2 / KW];
+                        const uint32_t A[4] = {hmul2(x[gr][0][2 * u], s0), hmul2(x[gr][1][2 * u], s1),
+                                               hmul2(x[gr][0][2 * u + 1], s0), hmul2(x[gr][1][2 * u + 1], s1)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816(sc[gr][nt], A, qf[nt].x, qf[nt].y);
                     }
                 }
             }
@@ -462,21 +474,6 @@ __global__ void __launch_bounds__(Shape<NT>::threads, 2) k_paged_attn(const Attn
             if (lane == 0) mbar_arrive(&empty[stage]);
         }
 
-        // join the warps: rows' (m, l) and O through shared memory
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-#pragma unroll
-                for (int x = 4; x < 32; x <<= 1) l[nt][z] += __shfl_xor_sync(0xffffffffu, l[nt][z], x);
-                const int row = nt * 8 + 2 * t + z;
-                float* dst = so + (warp * RB + row) * (D + 4) + g * (D / 8);
-#pragma unroll
-                for (int j = 0; j < KS; j += 2)  // tiles j: channels 2j, 2j + 1 of the lane's D/8
-                    *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(o[nt][j][z], o[nt][j][z + 2], o[nt][j + 1][z], o[nt][j + 1][z + 2]);
-                if (g == 0) sml[warp * RB + row] = make_float2(m[nt][z], l[nt][z]);
-            }
-        asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
         const bool whole = un == sg.u;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (at != g0);
         // the first piece says where all are: its slot, the block of the last one, and whose rows
@@ -492,33 +489,57 @@ __global__ void __launch_bounds__(Shape<NT>::threads, 2) k_paged_attn(const Attn
                 a.rec[blockIdx.x] = rec;
             }
         }
-        for (int it = threadIdx.x; it < RB * (D / 4); it += W * 32) {
-            const int row = it / (D / 4), c4 = it % (D / 4) * 4;
-            if (row >= rw.R) break;
-            float M = -INFINITY, LL = 0.0f;
+        // join the warps: (m, l) and O of 4 rows at a time through shared memory
 #pragma unroll
-            for (int w = 0; w < W; ++w) M = fmaxf(M, sml[w * RB + row].x);
-            float4 acc = make_float4(0, 0, 0, 0);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float2 ml = sml[w * RB + row];
-                if (ml.y == 0.0f) continue;  // saw nothing; a row of NaN scores has m = -inf, l = NaN
-                const float f = ex2(ml.x - M);
-                const float4 x = *reinterpret_cast<const float4*>(so + (w * RB + row) * (D + 4) + c4);
-                LL += f * ml.y;
-                acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+            for (int z = 0; z < 2; ++z)
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[nt][z] += __shfl_xor_sync(0xffffffffu, l[nt][z], x);
+#pragma unroll
+        for (int part = 0; part < 2 * NT; ++part) {
+            const int nt = part / 2;
+            if (part * 4 >= rw.R) break;
+            if (t >> 1 == (part & 1)) {
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const int row = warp * 4 + 2 * (t & 1) + z;
+                    float* dst = so + row * (D + 4) + g * (D / 8);
+#pragma unroll
+                    for (int j = 0; j < KS; j += 2)  // tiles j: channels 2j, 2j + 1 of the lane's D/8
+                        *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(o[nt][j][z], o[nt][j][z + 2], o[nt][j + 1][z], o[nt][j + 1][z + 2]);
+                    if (g == 0) sml[row] = make_float2(m[nt][z], l[nt][z]);
+                }
             }
-            if (whole) {
-                const int64_t grow = (int64_t)(rw.c0 + row / G) * a.c.Hq + h * G + row % G;
-                const float inv = LL == 0.0f ? 0.0f : a.out_scale / LL;
-                store4<BF>(a.out + grow * D + c4, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-                if (c4 == 0 && a.lse) a.lse[grow] = LL == 0.0f ? -INFINITY : (M + log2f(LL)) * kLn2;
-            } else {
-                *reinterpret_cast<float4*>(a.part + (slot * RB + row) * D + c4) = acc;
-                if (c4 == 0) a.pml[slot * RB + row] = make_float2(M, LL);
+            asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
+            for (int it = threadIdx.x; it < 4 * (D / 4); it += W * 32) {
+                const int r4 = it / (D / 4), row = part * 4 + r4, c4 = it % (D / 4) * 4;
+                if (row >= rw.R) break;
+                float M = -INFINITY, LL = 0.0f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) M = fmaxf(M, sml[w * 4 + r4].x);
+                float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const float2 ml = sml[w * 4 + r4];
+                    if (ml.y == 0.0f) continue;  // saw nothing; a row of NaN scores has m = -inf, l = NaN
+                    const float f = ex2(ml.x - M);
+                    const float4 x = *reinterpret_cast<const float4*>(so + (w * 4 + r4) * (D + 4) + c4);
+                    LL += f * ml.y;
+                    acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+                }
+                if (whole) {
+                    const int64_t grow = (int64_t)(rw.c0 + row / G) * a.c.Hq + h * G + row % G;
+                    const float inv = LL == 0.0f ? 0.0f : a.out_scale / LL;
+                    store4<BF>(a.out + grow * D + c4, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+                    if (c4 == 0 && a.lse) a.lse[grow] = LL == 0.0f ? -INFINITY : (M + log2f(LL)) * kLn2;
+                } else {
+                    *reinterpret_cast<float4*>(a.part + (slot * RB + row) * D + c4) = acc;
+                    if (c4 == 0) a.pml[slot * RB + row] = make_float2(M, LL);
+                }
             }
+            asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
     }
     if (threadIdx.x == 0 && *dead) set_status(a.status, KVQ_STATUS_WAIT_TIMEOUT);
 }
@@ -684,7 +705,7 @@ int run_few(const AttnArgs& a, const Plan& p, int B, int rows, cudaStream_t st) 
     auto* kern = k_paged_attn<D, NT, BF>;
     static SmemOptIn opt;
     if (int e = opt.set((const void*)kern, L::total)) return e;
-    kern<<<p.S, Shape<NT>::threads, L::total, st>>>(a, B);
+    kern<<<p.S, kFewThreads<NT>, L::total, st>>>(a, B);
     cudaError_t ce = cudaGetLastError();
     if (ce || !p.join || p.S == 1) return record_cuda(ce);
     // its launch overlaps the main kernel's end; it waits for that before it reads anything
