@@ -506,22 +506,23 @@ class PagedCache:
         self.dtype = torch.bfloat16 if cfg.dtype else torch.float16
         self.struct = PagedStruct(pool.data_ptr(), self.status.data_ptr())
         self.args = byref(cfg), byref(self.struct)
+        self.q_row, self.kv_row, self.width = (cfg.Hq, cfg.D), (cfg.Hkv, cfg.D), cfg.max_pages
 
     def nbytes(self) -> int:
         return self.pool.numel()
 
 
-_i32 = _raw_stream = _current = None
+_i32 = _f32 = _f64 = _raw_stream = _current = None
 
 
 def _torch():
     """torch, and the names that the calls below need every time (a call costs a few microseconds
     of host time, as much as the smallest kernels take)."""
-    global _i32, _raw_stream, _current
+    global _i32, _f32, _f64, _raw_stream, _current
     import torch
     if _i32 is None:
         _raw_stream, _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-        _i32 = torch.int32
+        _i32, _f32, _f64 = torch.int32, torch.float32, torch.float64
     return torch
 
 
@@ -552,6 +553,8 @@ def _rows(where, name, t, shape, dtype, i):
         raise ValueError(f"{where}: {name} is {tuple(t.shape)} {t.dtype} on {t.device}, not "
                          f"{shape} {dtype} on the call's device")
     n, heads, d = shape
+    if t.is_contiguous():
+        return heads * d
     row, head, one = t.stride()
     if (one != 1 and d > 1) or (head != d and heads > 1):
         raise ValueError(f"{where}: {name}'s heads and channels are not contiguous")
@@ -573,9 +576,8 @@ def kvq_paged_get_status(cache: PagedCache, stream=None) -> int:
 
 def _table(where, cache, table, B):
     _ints(where, cache.index, table)
-    if table.shape != (B, cache.cfg.max_pages):
-        raise ValueError(f"{where}: block_table is {tuple(table.shape)}, not "
-                         f"{(B, cache.cfg.max_pages)}")
+    if table.shape != (B, cache.width):
+        raise ValueError(f"{where}: block_table is {tuple(table.shape)}, not {(B, cache.width)}")
 
 
 def kvq_page_plan(cache: PagedCache, lens, n_new, block_table, free_pages, n_free, cu_new, len_out,
@@ -605,22 +607,21 @@ def kvq_page_release(cache: PagedCache, lens, done, block_table, free_pages, n_f
 
 
 def kvq_paged_append(cache: PagedCache, k, v, slots, stream=None) -> None:
-    w, c, i = "kvq_paged_append", cache.cfg, cache.index
-    n = slots.numel()
+    w, i, n = "kvq_paged_append", cache.index, slots.numel()
     _ints(w, i, slots)
-    shape = n, c.Hkv, c.D
+    shape = n, *cache.kv_row
     ks, vs = _rows(w, "k", k, shape, cache.dtype, i), _rows(w, "v", v, shape, cache.dtype, i)
     _call(w, load().kvq_paged_append, i, stream, *cache.args, k.data_ptr(), ks, v.data_ptr(), vs,
           slots.data_ptr(), n)
 
 
 def kvq_paged_dequantize(cache: PagedCache, slots, khat, vhat, stream=None) -> None:
-    w, c, i = "kvq_paged_dequantize", cache.cfg, cache.index
-    n = slots.numel()
+    w, i, n = "kvq_paged_dequantize", cache.index, slots.numel()
     _ints(w, i, slots)
-    shape = n, c.Hkv, c.D
-    if (_rows(w, "khat", khat, shape, cache.dtype, i) != c.Hkv * c.D
-            or _rows(w, "vhat", vhat, shape, cache.dtype, i) != c.Hkv * c.D):
+    shape = n, *cache.kv_row
+    _rows(w, "khat", khat, shape, cache.dtype, i)
+    _rows(w, "vhat", vhat, shape, cache.dtype, i)
+    if not (khat.is_contiguous() and vhat.is_contiguous()):
         raise ValueError(f"{w}: an output is not contiguous")
     _call(w, load().kvq_paged_dequantize, i, stream, *cache.args, slots.data_ptr(), n,
           khat.data_ptr(), vhat.data_ptr())
@@ -638,13 +639,13 @@ def kvq_paged_attention(cache: PagedCache, q, cu_q, lens, block_table, max_q: in
                         sm_scale: float, out, workspace=None, window: int = 0, lse=None,
                         splits: int = 0, stream=None) -> None:
     """cu_q: int32 [B + 1], or None for one query per request."""
-    w, c, i = "kvq_paged_attention", cache.cfg, cache.index
-    B, n = lens.numel(), q.shape[0]
+    w, i, B, n = "kvq_paged_attention", cache.index, lens.numel(), q.shape[0]
     _ints(w, i, lens)
     _table(w, cache, block_table, B)
-    shape = n, c.Hq, c.D
+    shape = n, *cache.q_row
     qs = _rows(w, "q", q, shape, cache.dtype, i)
-    if _rows(w, "out", out, shape, cache.dtype, i) != c.Hq * c.D:
+    _rows(w, "out", out, shape, cache.dtype, i)
+    if not out.is_contiguous():
         raise ValueError(f"{w}: out is not contiguous")
     cu = l = ws = None
     wb = 0
@@ -654,7 +655,7 @@ def kvq_paged_attention(cache: PagedCache, q, cu_q, lens, block_table, max_q: in
             raise ValueError(f"{w}: cu_q has {cu_q.numel()} entries for {B} requests")
         cu = cu_q.data_ptr()
     if lse is not None:
-        if (lse.dtype is not _torch().float32 or lse.get_device() != i or lse.shape != shape[:2]
+        if (lse.dtype is not _f32 or lse.get_device() != i or lse.shape != shape[:2]
                 or not lse.is_contiguous()):
             raise ValueError(f"{w}: lse is a contiguous float32 tensor {shape[:2]} on q's device")
         l = lse.data_ptr()
@@ -668,29 +669,32 @@ def kvq_paged_attention(cache: PagedCache, q, cu_q, lens, block_table, max_q: in
 
 
 def make_rope_cfg(Hq, Hkv, D, rot_dim, pair_axis, dtype, adjacent=False) -> RopeCfg:
-    """pair_axis: the axis (0, 1, ...) of each of the rot_dim/2 pairs, as a list."""
+    """pair_axis: the axis (0, 1, ...) of each of the rot_dim/2 pairs, as a list.  The result is
+    not to be changed."""
     axes = [int(x) for x in pair_axis]
     if len(axes) != rot_dim // 2 or len(axes) > 128 or min(axes, default=-1) < 0 or max(axes) > 7:
         raise ValueError(f"make_rope_cfg: pair_axis names an axis (0 .. 7) for each of the "
                          f"{rot_dim // 2} pairs")
-    return RopeCfg(Hq, Hkv, D, rot_dim, _dtype_code(dtype), int(bool(adjacent)), max(axes) + 1,
-                   (c_uint8 * 128)(*axes))
+    cfg = RopeCfg(Hq, Hkv, D, rot_dim, _dtype_code(dtype), int(bool(adjacent)), max(axes) + 1,
+                  (c_uint8 * 128)(*axes))
+    _torch()
+    cfg.py = Hq, Hkv, D, max(axes) + 1, rot_dim // 2, dtype  # for kvq_rope's checks
+    return cfg
 
 
 def kvq_rope(cfg: RopeCfg, q, k, positions, freqs, q_out, k_out, inverse=False,
              stream=None) -> None:
     """q, k [n, heads, D] (k may be None when cfg.Hkv is 0), positions int32 [axes, n], freqs
     float64 [rot_dim / 2]; q_out and k_out may be q and k."""
-    torch = _torch()
-    w, n, i, Hkv, d = "kvq_rope", q.shape[0], q.get_device(), cfg.Hkv, cfg.D
-    dtype = (torch.float16, torch.bfloat16, torch.float32)[cfg.dtype]
+    w, n, i = "kvq_rope", q.shape[0], q.get_device()
+    Hq, Hkv, d, axes, half, dtype = cfg.py
     _ints(w, i, positions)
-    if positions.shape != (cfg.axes, n) and not (cfg.axes == 1 and positions.numel() == n):
-        raise ValueError(f"{w}: positions is {tuple(positions.shape)}, not {(cfg.axes, n)}")
-    if (freqs.dtype is not torch.float64 or freqs.numel() != cfg.rot_dim // 2
-            or freqs.get_device() != i or not freqs.is_contiguous()):
-        raise ValueError(f"{w}: freqs is a float64 tensor of {cfg.rot_dim // 2} on q's device")
-    shape = n, cfg.Hq, d
+    if positions.shape != (axes, n) and not (axes == 1 and positions.numel() == n):
+        raise ValueError(f"{w}: positions is {tuple(positions.shape)}, not {(axes, n)}")
+    if (freqs.dtype is not _f64 or freqs.numel() != half or freqs.get_device() != i
+            or not freqs.is_contiguous()):
+        raise ValueError(f"{w}: freqs is a float64 tensor of {half} on q's device")
+    shape = n, Hq, d
     qs, qos = _rows(w, "q", q, shape, dtype, i), _rows(w, "q_out", q_out, shape, dtype, i)
     kp = kop = None
     ks = kos = 0
