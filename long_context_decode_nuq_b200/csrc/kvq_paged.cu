@@ -47,10 +47,6 @@ struct PlanArgs {
 
 constexpr int kPlanThreads = 1024;
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-
 // Inclusive prefix sums of a and b over the block; the totals in *ta, *tb.
 __device__ inline void scan2(long long& a, long long& b, long long (&sm)[2][32], long long* ta,
                              long long* tb) {

@@ -62,6 +62,10 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // One 16-bit value of the cache's type, either way.
 template <bool BF>
 __device__ __forceinline__ float lo16(uint32_t w) {

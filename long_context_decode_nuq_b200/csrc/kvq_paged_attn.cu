@@ -17,6 +17,10 @@ namespace {
 // pieces, and k_paged_join adds them up in order, told by the block of the first piece where they
 // are.
 //
+// Where the work is short (CL), a cluster of C blocks takes one (request, kv head) instead, an equal
+// part of its units each, and adds the parts through distributed shared memory: no search for the
+// block's place, no workspace and no second kernel (one request of 1000 tokens: @CL@).
+//
 // In a block one warp brings the codes: a stage is 32 tokens for each of the W others, a lane one
 // group of 16 tokens, which is one contiguous run of the pool.  The W warps take 32 tokens each,
 // keep running maxima and sums of the rows and join at the end of a piece.
@@ -106,7 +110,7 @@ __device__ __forceinline__ bool wait_or(uint64_t* bar, uint32_t parity, volatile
     return false;
 }
 
-template <int D, int NT, bool BF>
+template <int D, int NT, bool BF, bool CL>
 __global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArgs a, int B) {
     using L = FewSmem<D, NT>;
     constexpr int W = L::W, ST = L::ST, RB = L::RB;
@@ -132,8 +136,21 @@ __global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArg
         fence_mbar_init();
     }
     // where this block's units begin: prefix sums of the requests' units
-    int64_t base = 0, T;  // units before request b; all units
-    int b = 0;
+    int64_t base = 0, T = 0;  // units before request b; all units
+    int b = 0, N = 1;
+    int64_t g0 = 0, g1 = 0;
+    if constexpr (CL) {
+        const int C = a.S, seg = blockIdx.x / C, rank = blockIdx.x % C;
+        b = seg / Hkv;
+        const Seg s = seg_of(a, b);
+        if (seg % Hkv == 0 && rank == 0 && threadIdx.x == 0 && (s.rw.n > s.rw.nq || s.rw.len > s.rw.kv))
+            set_status(a.status, KVQ_STATUS_LEN_OVERFLOW);
+        if (s.u == 0) return;  // no rows: the whole cluster leaves
+        // positions within the request, as if it were the first: kv heads one after the other
+        const int64_t at = (int64_t)(seg % Hkv) * s.u;
+        g0 = at + (int64_t)s.u * rank / C, g1 = at + (int64_t)s.u * (rank + 1) / C;
+        __syncthreads();
+    } else {
     auto report = [&](const Seg& s, int r) {  // by block 0, for every request
         if (s.rw.n > s.rw.nq || s.rw.len > s.rw.kv) set_status(a.status, KVQ_STATUS_LEN_OVERFLOW);
         if (s.u == 0 && a.rec && a.by_request)
@@ -195,12 +212,13 @@ __global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArg
     }
     // every block has started by the time this takes effect: k_paged_join may take free places
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int N = (int)min((int64_t)gridDim.x, T);  // blocks that have units
+    N = (int)min((int64_t)gridDim.x, T);  // blocks that have units
     if ((int)blockIdx.x >= N) {
         if (a.rec && !a.by_request && threadIdx.x == 0) a.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
         return;
     }
-    const int64_t g0 = share(T, blockIdx.x, N), g1 = share(T, blockIdx.x + 1, N);
+    g0 = share(T, blockIdx.x, N), g1 = share(T, blockIdx.x + 1, N);
+    }
     Seg sg = seg_of(a, b);
 
     // the pieces of [g0, g1): request b, kv head h, units [u0, u0 + un)
@@ -474,10 +492,10 @@ __global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArg
             if (lane == 0) mbar_arrive(&empty[stage]);
         }
 
-        const bool whole = un == sg.u;
+        const bool whole = !CL && un == sg.u;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (at != g0);
         // the first piece says where all are: its slot, the block of the last one, and whose rows
-        if (a.rec && threadIdx.x == 0) {
+        if (!CL && a.rec && threadIdx.x == 0) {
             int4 rec = make_int4(-1, 0, 0, 0);
             if (u0 == 0 && !whole) {
                 const int64_t end = at + sg.u;
@@ -533,6 +551,9 @@ __global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArg
                     const float inv = LL == 0.0f ? 0.0f : a.out_scale / LL;
                     store4<BF>(a.out + grow * D + c4, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
                     if (c4 == 0 && a.lse) a.lse[grow] = LL == 0.0f ? -INFINITY : (M + log2f(LL)) * kLn2;
+                } else if (CL) {  // the ring is no longer read
+                    *reinterpret_cast<float4*>(smem + (row * D + c4) * 4) = acc;
+                    if (c4 == 0) *reinterpret_cast<float2*>(smem + RB * D * 4 + row * 8) = make_float2(M, LL);
                 } else {
                     *reinterpret_cast<float4*>(a.part + (slot * RB + row) * D + c4) = acc;
                     if (c4 == 0) a.pml[slot * RB + row] = make_float2(M, LL);
@@ -540,6 +561,44 @@ __global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArg
             }
             asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
         }
+    }
+    if constexpr (CL) {
+        const int C = a.S, rank = blockIdx.x % C, hh = blockIdx.x / C % Hkv;
+        const Rows& rw = sg.rw;
+        if (g0 >= g1)  // no units: an empty part
+            for (int row = threadIdx.x; row < RB; row += W * 32)
+                *reinterpret_cast<float2*>(smem + RB * D * 4 + row * 8) = make_float2(-INFINITY, 0.0f);
+        __syncwarp();
+        cluster_sync();
+        // part p of a row from block p, in that order; the rows' quarters over the blocks' threads
+        const uint32_t here = smem_u32(smem);
+        for (int it = rank * (W * 32) + threadIdx.x; it < rw.R * (D / 4); it += C * W * 32) {
+            const int row = it / (D / 4), c4 = it % (D / 4) * 4;
+            float M = -INFINITY, LL = 0.0f;
+            float4 acc = make_float4(0, 0, 0, 0);
+            for (int p = 0; p < C; ++p) {
+                float2 ml;
+                float4 x;
+                uint32_t from;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(here), "r"(p));
+                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(ml.x), "=f"(ml.y) : "r"(from + RB * D * 4 + row * 8));
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                             : "r"(from + (row * D + c4) * 4));
+                if (ml.y == 0.0f) continue;
+                const float mn = fmaxf(M, ml.x), f = LL == 0.0f ? 0.0f : ex2(M - mn), e = ex2(ml.x - mn);
+                LL = LL * f + e * ml.y;
+                acc.x = acc.x * f + e * x.x, acc.y = acc.y * f + e * x.y;
+                acc.z = acc.z * f + e * x.z, acc.w = acc.w * f + e * x.w;
+                M = mn;
+            }
+            const int64_t grow = (int64_t)(rw.c0 + row / G) * a.c.Hq + hh * G + row % G;
+            const float inv = LL == 0.0f ? 0.0f : a.out_scale / LL;
+            store4<BF>(a.out + grow * D + c4, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            if (c4 == 0 && a.lse) a.lse[grow] = LL == 0.0f ? -INFINITY : (M + log2f(LL)) * kLn2;
+        }
+        __syncwarp();
+        cluster_sync();  // no block leaves while another reads its part
     }
     if (threadIdx.x == 0 && *dead) set_status(a.status, KVQ_STATUS_WAIT_TIMEOUT);
 }
@@ -634,7 +693,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const AttnArgs
 struct Plan {
     int nt;   // 8-row tiles of k_paged_attn; 0: the chunk kernel
     int nrb;  // chunk kernel: row blocks
-    int S;    // chunk kernel: splits;  k_paged_attn: blocks
+    int S;    // chunk kernel: splits;  k_paged_attn: blocks, or blocks of a cluster
+    bool cluster;
     bool join;
 };
 
@@ -661,7 +721,7 @@ Plan plan_of(const kvq_paged_cfg* c, int B, int max_q, int max_len, int splits, 
     // no row block sees more tokens than this
     int64_t span = max_len;
     if (window > 0 && span > (int64_t)window + max_q + 128) span = (int64_t)window + max_q + 128;
-    Plan p;
+    Plan p{};
     p.nt = R <= 8 ? 1 : R <= kFewRows ? 2 : 0;
     p.nrb = p.nt ? 1 : (int)((R + kChunkRows - 1) / kChunkRows);
     const int64_t units = (int64_t)B * c->Hkv * p.nrb;
@@ -675,9 +735,20 @@ Plan plan_of(const kvq_paged_cfg* c, int B, int max_q, int max_len, int splits, 
         p.join = p.S > 1;
         return p;
     }
+    p.cluster = false;
+    const int64_t per = (span + kUnit - 1) / kUnit + 1;  // units of one, at most
+    if (!splits) {
+        // clusters where they fill no more than a wave and no block gets over 512 tokens
+        int C = 8;
+        while (C > 1 && (units * C > 2 * kSms || C / 2 >= per)) C /= 2;
+        if (units * C <= 2 * kSms && per <= 8 * C) {
+            p.cluster = true, p.S = C, p.join = false;
+            return p;
+        }
+    }
     // two blocks are resident on an SM: one wave of equal shares, or fewer where there are not
     // that many units of 64 tokens
-    const int64_t most = units * ((span + kUnit - 1) / kUnit + 1);
+    const int64_t most = units * per;
     int64_t N = splits ? units * splits : 2 * kSms;
     if (N > most) N = most;
     p.S = (int)(N > (1 << 20) ? 1 << 20 : N);
@@ -702,7 +773,24 @@ size_t ws_bytes(const kvq_paged_cfg* cfg, const Plan& p, int32_t B, int32_t tota
 template <int D, int NT, bool BF>
 int run_few(const AttnArgs& a, const Plan& p, int B, int rows, cudaStream_t st) {
     using L = FewSmem<D, NT>;
-    auto* kern = k_paged_attn<D, NT, BF>;
+    if (p.cluster) {
+        auto* kern = k_paged_attn<D, NT, BF, true>;
+        static SmemOptIn opt;
+        if (int e = opt.set((const void*)kern, L::total)) return e;
+        cudaLaunchConfig_t lc = {};
+        lc.gridDim = dim3((unsigned)(p.S * B * a.c.Hkv));
+        lc.blockDim = dim3(kFewThreads<NT>);
+        lc.dynamicSmemBytes = L::total;
+        lc.stream = st;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = p.S;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        lc.attrs = at;
+        lc.numAttrs = 1;
+        return record_cuda(cudaLaunchKernelEx(&lc, kern, (const AttnArgs)a, B));
+    }
+    auto* kern = k_paged_attn<D, NT, BF, false>;
     static SmemOptIn opt;
     if (int e = opt.set((const void*)kern, L::total)) return e;
     kern<<<p.S, kFewThreads<NT>, L::total, st>>>(a, B);
