@@ -94,6 +94,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
     uint32_t *s_tok = s_plan, *s_page = s_plan + chunk, *s_len = s_plan + 2 * chunk;  // length: top bit, accepted
     const int rank = blockIdx.x, nc = gridDim.x;  // the grid is one cluster
     const int lp = 31 - __clz(a.P), pm = a.P - 1;
+    let_next();
+    after_previous();
     const int n_free = min(max(*a.n_free, 0), a.num_pages);
     long long tok0 = 0, page0 = 0;
     int bad = 0;
@@ -202,26 +204,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
 }
 
 template <int ITEMS>
-cudaError_t launch_plan(const PlanArgs& a, int blocks, int threads, cudaStream_t st) {
+int launch_plan(const PlanArgs& a, int blocks, int threads, cudaStream_t st) {
     const size_t smem = (size_t)threads * ITEMS * 12;
     static SmemOptIn opt;
-    if (ITEMS > 1 && opt.set((const void*)k_page_plan<ITEMS>, kPlanThreads * ITEMS * 12)) return cudaGetLastError();
-    if (blocks == 1) {
-        k_page_plan<ITEMS><<<1, threads, smem, st>>>(a);
-        return cudaGetLastError();
-    }
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(blocks);
-    lc.blockDim = dim3(threads);
-    lc.dynamicSmemBytes = smem;
-    lc.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = blocks;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    lc.attrs = at;
-    lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, k_page_plan<ITEMS>, (const PlanArgs)a);
+    if (int e = ITEMS > 1 ? opt.set((const void*)k_page_plan<ITEMS>, kPlanThreads * ITEMS * 12) : KVQ_OK) return e;
+    return launch_overlapped(k_page_plan<ITEMS>, dim3(blocks), threads, smem, blocks, st, a);
 }
 
 // Release: the same walk over requests, one block; pages pushed in request order.
@@ -231,6 +218,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     __shared__ uint32_t s_page[kPlanThreads];
     __shared__ long long s_scan[2][32];
     const int tid = threadIdx.x, nt = blockDim.x;
+    let_next();
+    after_previous();
     const int n_free = min(max(*n_free_p, 0), num_pages);
     long long page0 = 0;
     for (int base = 0; base < B; base += nt) {
@@ -371,6 +360,8 @@ __global__ void __launch_bounds__(kAppThreads)
                    const uint16_t* __restrict__ k, int64_t ks, const uint16_t* __restrict__ v,
                    int64_t vs, const int32_t* __restrict__ slots, int n, int tokens) {
     const bool val = blockIdx.z;
+    let_next();
+    after_previous();
     const Walk w = walk_of<D, 16>(cfg, n, tokens, val);
     const uint16_t* src = (val ? v : k) + w.r * 16;
     const int64_t stride = val ? vs : ks;
@@ -406,6 +397,8 @@ __global__ void __launch_bounds__(kAppThreads)
                     const int32_t* __restrict__ slots, int n, uint16_t* __restrict__ khat,
                     uint16_t* __restrict__ vhat, int tokens) {
     const bool val = blockIdx.z;
+    let_next();
+    after_previous();
     const Walk w = walk_of<D, 8>(cfg, n, tokens, val);
     uint16_t* dst = (val ? vhat : khat) + w.r * 8;
     const int64_t stride = (int64_t)cfg.Hkv * D;
@@ -510,7 +503,7 @@ int kvq_page_plan(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_
     const int threads = most >= kPlanThreads ? kPlanThreads : (most + 31) / 32 * 32;
     const int blocks = capacity > 4096 ? 8 : 1;
     cudaStream_t st = (cudaStream_t)stream;
-    return record_cuda(B > threads ? launch_plan<4>(a, blocks, threads, st) : launch_plan<1>(a, blocks, threads, st));
+    return B > threads ? launch_plan<4>(a, blocks, threads, st) : launch_plan<1>(a, blocks, threads, st);
 }
 
 int kvq_page_release(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_t B,
@@ -521,10 +514,8 @@ int kvq_page_release(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int
     if (!cache || !cache->status || !len || !done || !block_table || !free_pages || !n_free)
         return KVQ_ERR_NULL;
     if (B < 1 || B > (1 << 20)) return KVQ_ERR_SHAPE;
-    k_page_release<<<1, kPlanThreads, 0, (cudaStream_t)stream>>>(
-        B, cfg->page_tokens, cfg->num_pages, cfg->max_pages, len, done, block_table, free_pages,
-        n_free, cache->status);
-    return record_cuda(cudaGetLastError());
+    return launch_overlapped(k_page_release, dim3(1), kPlanThreads, 0, 1, (cudaStream_t)stream, B, cfg->page_tokens,
+                             cfg->num_pages, cfg->max_pages, len, done, block_table, free_pages, n_free, cache->status);
 }
 
 int kvq_paged_append(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, const void* k,
@@ -544,10 +535,8 @@ int kvq_paged_append(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, con
                               : (bf ? k_paged_append<128, true> : k_paged_append<128, false>);
     int tokens;
     const dim3 grid = app_grid(cfg, 16, n, &tokens);
-    kern<<<grid, kAppThreads, 0, (cudaStream_t)stream>>>(
-        *cfg, cache->pool, cache->status, (const uint16_t*)k, k_stride, (const uint16_t*)v,
-        v_stride, slots, n, tokens);
-    return record_cuda(cudaGetLastError());
+    return launch_overlapped(kern, grid, kAppThreads, 0, 1, (cudaStream_t)stream, *cfg, cache->pool, cache->status,
+                             (const uint16_t*)k, k_stride, (const uint16_t*)v, v_stride, slots, n, tokens);
 }
 
 int kvq_paged_dequantize(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache,
@@ -564,9 +553,8 @@ int kvq_paged_dequantize(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache,
                               : (bf ? k_paged_dequant<128, true> : k_paged_dequant<128, false>);
     int tokens;
     const dim3 grid = app_grid(cfg, 8, n, &tokens);
-    kern<<<grid, kAppThreads, 0, (cudaStream_t)stream>>>(
-        *cfg, cache->pool, cache->status, slots, n, (uint16_t*)khat, (uint16_t*)vhat, tokens);
-    return record_cuda(cudaGetLastError());
+    return launch_overlapped(kern, grid, kAppThreads, 0, 1, (cudaStream_t)stream, *cfg, (const uint8_t*)cache->pool,
+                             cache->status, slots, n, (uint16_t*)khat, (uint16_t*)vhat, tokens);
 }
 
 }  // extern "C"

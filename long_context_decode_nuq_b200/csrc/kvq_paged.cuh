@@ -66,6 +66,12 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// Kernels of the paged cache are launched with leave to start before the one ahead in the stream
+// has ended: after_previous waits until that has, and its writes are seen; before it nothing of
+// the caller's memory is touched, and no thread returns.  let_next gives the same leave on.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // One 16-bit value of the cache's type, either way.
 template <bool BF>
 __device__ __forceinline__ float lo16(uint32_t w) {
@@ -104,6 +110,25 @@ struct SmemOptIn {
         return KVQ_OK;
     }
 };
+// Launch in clusters of `cluster` blocks, overlapping the start with the kernel ahead.
+template <typename... P, typename... A>
+int launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st,
+                      A... args) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = grid;
+    lc.blockDim = dim3(threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    lc.attrs = at;
+    lc.numAttrs = cluster > 1 ? 2 : 1;
+    return record_cuda(cudaLaunchKernelEx(&lc, kernel, static_cast<P>(args)...));
+}
 int check_paged_cfg(const kvq_paged_cfg* cfg);
 int check_paged_cache(const kvq_paged_cache* cache);
 }  // namespace kvq_host

@@ -135,6 +135,8 @@ __global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArg
         for (int i = 0; i < ST; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], W);
         fence_mbar_init();
     }
+    let_next();
+    after_previous();
     // where this block's units begin: prefix sums of the requests' units
     int64_t base = 0, T = 0;  // units before request b; all units
     int b = 0, N = 1;
@@ -210,8 +212,6 @@ __global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArg
         __syncthreads();
         if (at < T) base = s_start[0], b = (int)s_start[1];
     }
-    // every block has started by the time this takes effect: k_paged_join may take free places
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     N = (int)min((int64_t)gridDim.x, T);  // blocks that have units
     if ((int)blockIdx.x >= N) {
         if (a.rec && !a.by_request && threadIdx.x == 0) a.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -611,7 +611,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_paged_join(const AttnArgs a
     __shared__ float s_o[kJoinWarps][D];
     __shared__ float2 s_ml[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    let_next();
+    after_previous();
     const int4 rec = a.rec[blockIdx.x];
     const int w1 = rec.x, w0 = rec.y >> 1, h = rec.w >> 8, R = rec.w & 255;
     if (w1 < 0 || row >= R) return;
@@ -661,6 +662,8 @@ template <int D, bool BF>
 __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const AttnArgs a) {
     const int h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31;
     const int G = a.c.Hq / a.c.Hkv;
+    let_next();
+    after_previous();
     const Rows rw = rows_of(a, b);
     const int64_t nrow = (int64_t)a.total_q * a.c.Hq;
     const int r = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
@@ -777,36 +780,14 @@ int run_few(const AttnArgs& a, const Plan& p, int B, int rows, cudaStream_t st) 
         auto* kern = k_paged_attn<D, NT, BF, true>;
         static SmemOptIn opt;
         if (int e = opt.set((const void*)kern, L::total)) return e;
-        cudaLaunchConfig_t lc = {};
-        lc.gridDim = dim3((unsigned)(p.S * B * a.c.Hkv));
-        lc.blockDim = dim3(kFewThreads<NT>);
-        lc.dynamicSmemBytes = L::total;
-        lc.stream = st;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = p.S;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        lc.attrs = at;
-        lc.numAttrs = 1;
-        return record_cuda(cudaLaunchKernelEx(&lc, kern, (const AttnArgs)a, B));
+        return launch_overlapped(kern, dim3((unsigned)(p.S * B * a.c.Hkv)), kFewThreads<NT>, L::total, p.S, st, a, B);
     }
     auto* kern = k_paged_attn<D, NT, BF, false>;
     static SmemOptIn opt;
     if (int e = opt.set((const void*)kern, L::total)) return e;
-    kern<<<p.S, kFewThreads<NT>, L::total, st>>>(a, B);
-    cudaError_t ce = cudaGetLastError();
-    if (ce || !p.join || p.S == 1) return record_cuda(ce);
-    // its launch overlaps the main kernel's end; it waits for that before it reads anything
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)records(&a.c, p, B), rows);
-    lc.blockDim = dim3(kJoinWarps * 32);
-    lc.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = at;
-    lc.numAttrs = 1;
-    return record_cuda(cudaLaunchKernelEx(&lc, k_paged_join<D, BF>, (const AttnArgs)a, L::RB));
+    const int e = launch_overlapped(kern, dim3(p.S), kFewThreads<NT>, L::total, 1, st, a, B);
+    if (e || !p.join || p.S == 1) return e;
+    return launch_overlapped(k_paged_join<D, BF>, dim3((unsigned)records(&a.c, p, B), rows), kJoinWarps * 32, 0, 1, st, a, L::RB);
 }
 
 int check_sizes(const kvq_paged_cfg* cfg, int32_t B, int32_t total_q, int32_t max_q,
@@ -883,9 +864,9 @@ int kvq_paged_attention(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, 
             auto* mk = cfg->D == 64 ? (bf ? k_paged_merge<64, true> : k_paged_merge<64, false>)
                                     : (bf ? k_paged_merge<128, true> : k_paged_merge<128, false>);
             const int64_t R = (int64_t)max_q * (cfg->Hq / cfg->Hkv);
-            mk<<<dim3((unsigned)((R + kMergeWarps - 1) / kMergeWarps), cfg->Hkv, B), kMergeWarps * 32, 0, st>>>(a);
+            return launch_overlapped(mk, dim3((unsigned)((R + kMergeWarps - 1) / kMergeWarps), cfg->Hkv, B), kMergeWarps * 32, 0, 1, st, a);
         }
-        return record_cuda(cudaGetLastError());
+        return KVQ_OK;
     }
     const int rows = max_q * (cfg->Hq / cfg->Hkv);
     if (cfg->D == 64)

@@ -165,6 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int s = blockIdx.x % a.S, rb = nrb - 1 - blockIdx.x / a.S, h = blockIdx.y, b = blockIdx.z;
     const int G = a.c.Hq / a.c.Hkv, P = a.c.page_tokens;
+    let_next();
+    after_previous();
     const Rows rw = rows_of(a, b);
     const int r0 = rb * kRows;
     if (threadIdx.x == 0 && h == 0 && blockIdx.x == 0 && (rw.n > rw.nq || rw.len > rw.kv))
@@ -502,8 +504,7 @@ int launch(const AttnArgs& a, int nrb, int B, cudaStream_t st) {
         return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
     }();
     if (regs * 4 < 2 * kRegSoft + kRegDeq + kRegIssue) return KVQ_ERR_UNSUPPORTED;
-    kern<<<dim3((unsigned)(a.S * nrb), a.c.Hkv, B), kThreads, smem, st>>>(a, nrb);
-    return record_cuda(cudaGetLastError());
+    return launch_overlapped(kern, dim3((unsigned)(a.S * nrb), a.c.Hkv, B), kThreads, smem, 1, st, a, nrb);
 }
 
 }  // namespace

@@ -80,6 +80,8 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeArgs a) {
     extern __shared__ float2 s_cs[];  // [tokens][pairs]
     const int half = a.c.rot_dim / 2, t0 = blockIdx.x * a.tokens;
     const int nt = min(a.tokens, a.n - t0);
+    let_next();
+    after_previous();
     for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
         const int p = i % half, t = t0 + i / half;
         const double two_pi = 6.283185307179586476925286766559;
@@ -164,9 +166,10 @@ extern "C" int kvq_rope(const kvq_rope_cfg* cfg, const void* q, int64_t q_stride
     const size_t smem = (size_t)a.tokens * (cfg->rot_dim / 2) * sizeof(float2);
     cudaStream_t st = (cudaStream_t)stream;
     const bool adj = cfg->adjacent;
-    auto go = [&](auto* adjk, auto* halfk) { (adj ? adjk : halfk)<<<grid, kRopeThreads, smem, st>>>(a); };
-    if (cfg->dtype == KVQ_F32) go(k_rope<float, Vec8<float>, true>, k_rope<float, Vec8<float>, false>);
-    else if (cfg->dtype == KVQ_BF16) go(k_rope<uint16_t, Vec16<true>, true>, k_rope<uint16_t, Vec16<true>, false>);
-    else go(k_rope<uint16_t, Vec16<false>, true>, k_rope<uint16_t, Vec16<false>, false>);
-    return record_cuda(cudaGetLastError());
+    auto go = [&](auto* adjk, auto* halfk) {
+        return launch_overlapped(adj ? adjk : halfk, grid, kRopeThreads, smem, 1, st, a);
+    };
+    if (cfg->dtype == KVQ_F32) return go(k_rope<float, Vec8<float>, true>, k_rope<float, Vec8<float>, false>);
+    if (cfg->dtype == KVQ_BF16) return go(k_rope<uint16_t, Vec16<true>, true>, k_rope<uint16_t, Vec16<true>, false>);
+    return go(k_rope<uint16_t, Vec16<false>, true>, k_rope<uint16_t, Vec16<false>, false>);
 }
