@@ -656,12 +656,47 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_paged_join(const AttnArgs a
     if (threadIdx.x == 0 && a.lse) a.lse[grow] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
+// Joins the chunk kernel's splits of a row, in split order: a warp per row.
+constexpr int kMergeWarps = 4;
+template <int D, bool BF>
+__global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const AttnArgs a) {
+    const int h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31;
+    const int G = a.c.Hq / a.c.Hkv;
+    let_next();
+    after_previous();
+    const Rows rw = rows_of(a, b);
+    const int64_t nrow = (int64_t)a.total_q * a.c.Hq;
+    const int r = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    if (r >= rw.R) return;
+    const int64_t grow = (int64_t)(rw.c0 + r / G) * a.c.Hq + h * G + r % G;
+    float M = -INFINITY;
+    for (int s = lane; s < a.S; s += 32) M = fmaxf(M, a.pml[s * nrow + grow].x);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    float L = 0.0f, acc[D / 32] = {};
+    for (int s = 0; s < a.S; ++s) {
+        const float2 ml = a.pml[s * nrow + grow];
+        if (ml.y == 0.0f) continue;  // an empty split; one of NaN scores has m = -inf, l = NaN
+        const float f = ex2(ml.x - M);
+        const float* x = a.part + (s * nrow + grow) * D + lane * (D / 32);
+        L += f * ml.y;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) acc[i] += f * x[i];
+    }
+    const float inv = L == 0.0f ? 0.0f : a.out_scale / L;
+    uint16_t* out = a.out + grow * D + lane * (D / 32);
+#pragma unroll
+    for (int i = 0; i < D / 32; i += 2)
+        *reinterpret_cast<uint32_t*>(out + i) = pack16<BF>(acc[i] * inv, acc[i + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[grow] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
 // ---------------------------------------------------------------------------------
 // Host: which kernel, blocks or splits, workspace.
 struct Plan {
     int nt;   // 8-row tiles of k_paged_attn; 0: the chunk kernel
-    int nrb;  // chunk kernel: row blocks of a request where a block takes one each, else 0
-    int S;    // blocks, or blocks of a cluster
+    int nrb;  // chunk kernel: row blocks
+    int S;    // chunk kernel: splits;  k_paged_attn: blocks, or blocks of a cluster
     bool cluster;
     bool join;
 };
@@ -669,10 +704,20 @@ struct Plan {
 constexpr int kSms = 148;
 // More rows of a kv head than this go to the chunk kernel.
 constexpr int kFewRows = 16;
-// What the chunk kernel's pieces cost, as steps of a block: the two of @PS@.
-constexpr int kPieceSteps = 10;
-// What `splits` may ask for at most, so that the workspace stays in bounds.
-constexpr int kMaxBlocks = 1024;
+
+// Splits of the chunk kernel: the least time of a model in which a block costs 6 us and 1.2 us per
+// 128 tokens, blocks run one per SM in waves, and a split writes and reads its part at 5 TB/s.
+int chunk_splits(const kvq_paged_cfg* c, int64_t units, int64_t tiles) {
+    int best = 1;
+    double least = 1e30;
+    for (int S = 1; S <= 32 && S <= tiles; ++S) {
+        const int64_t waves = (units * S + kSms - 1) / kSms;
+        double t = (double)waves * (6.0 + 1.2 * (double)((tiles + S - 1) / S));
+        if (S > 1) t += 4.0 + (double)units * S * kChunkRows * c->D * 8 / 5e6;
+        if (t < 0.98 * least) least = t, best = S;
+    }
+    return best;
+}
 
 Plan plan_of(const kvq_paged_cfg* c, int B, int max_q, int max_len, int splits, int window) {
     const int64_t R = (int64_t)max_q * (c->Hq / c->Hkv);
@@ -681,19 +726,16 @@ Plan plan_of(const kvq_paged_cfg* c, int B, int max_q, int max_len, int splits, 
     if (window > 0 && span > (int64_t)window + max_q + 128) span = (int64_t)window + max_q + 128;
     Plan p{};
     p.nt = R <= 8 ? 1 : R <= kFewRows ? 2 : 0;
-    const int64_t nrb = p.nt ? 1 : (R + kChunkRows - 1) / kChunkRows, units = (int64_t)B * c->Hkv * nrb;
-    if (p.nt == 0) {  // one block on an SM
-        const int64_t per = (span + kChunkTokens - 1) / kChunkTokens + 1;
-        // in steps: a row block each, in waves, against equal shares and their pieces
-        const bool even = units * per / kSms + kPieceSteps < (units + kSms - 1) / kSms * per;
-        if ((splits ? splits == 1 : !even) && units <= INT32_MAX) {
-            p.nrb = (int)nrb, p.S = (int)units;
-            return p;
+    p.nrb = p.nt ? 1 : (int)((R + kChunkRows - 1) / kChunkRows);
+    const int64_t units = (int64_t)B * c->Hkv * p.nrb;
+    if (p.nt == 0) {
+        p.S = splits ? splits : chunk_splits(c, units, (span + 127) / 128);
+        // the workspace is sized without the window, which must not raise the splits
+        if (!splits && span < max_len) {
+            const int S = chunk_splits(c, units, ((int64_t)max_len + 127) / 128);
+            if (S < p.S) p.S = S;
         }
-        int64_t N = splits ? units * splits : kSms;
-        if (N > units * per) N = units * per;
-        p.S = (int)(N > kMaxBlocks ? kMaxBlocks : N);
-        p.join = span > kChunkTokens - kGroup;
+        p.join = p.S > 1;
         return p;
     }
     p.cluster = false;
@@ -712,24 +754,22 @@ Plan plan_of(const kvq_paged_cfg* c, int B, int max_q, int max_len, int splits, 
     const int64_t most = units * per;
     int64_t N = splits ? units * splits : 2 * kSms;
     if (N > most) N = most;
-    p.S = (int)(N > kMaxBlocks ? kMaxBlocks : N);
+    p.S = (int)(N > (1 << 20) ? 1 << 20 : N);
     p.join = span > kUnit && !(splits == 1 && B == 1);
     return p;
 }
 
-// Records for the joins.  k_paged_attn: one per (request, kv head), or per block if those are fewer;
-// the chunk kernel: two entries per block.
+// Records of k_paged_attn for k_paged_join: one per (request, kv head), or per block if those are
+// fewer.
 int64_t records(const kvq_paged_cfg* cfg, const Plan& p, int32_t B) {
     const int64_t segs = (int64_t)B * cfg->Hkv;
-    return p.nt == 0 ? 2 * p.S : segs < p.S ? segs : p.S;
+    return segs < p.S ? segs : p.S;
 }
 
-// Rows of the pieces: two pieces a block.
-size_t piece_rows(const Plan& p) { return (size_t)2 * p.S * (p.nt ? 8 * p.nt : kChunkRows); }
-
-size_t ws_bytes(const kvq_paged_cfg* cfg, const Plan& p, int32_t B) {
+size_t ws_bytes(const kvq_paged_cfg* cfg, const Plan& p, int32_t B, int32_t total_q) {
     if (!p.join) return 0;
-    return piece_rows(p) * (cfg->D + 2) * 4 + (size_t)records(cfg, p, B) * 16;
+    if (p.nt == 0) return (size_t)p.S * total_q * cfg->Hq * (cfg->D + 2) * 4;
+    return (size_t)(2 * p.S) * 8 * p.nt * (cfg->D + 2) * 4 + (size_t)records(cfg, p, B) * 16;
 }
 
 // Few rows: the main kernel, and the join where a (request, kv head) may have been cut.
@@ -768,7 +808,7 @@ int kvq_paged_attention_workspace(const kvq_paged_cfg* cfg, int32_t B, int32_t t
     if (e) return e;
     if (!bytes) return KVQ_ERR_NULL;
     if ((e = check_sizes(cfg, B, total_q, max_q, max_len, splits))) return e;
-    *bytes = ws_bytes(cfg, plan_of(cfg, B, max_q, max_len, splits, 0), B);
+    *bytes = ws_bytes(cfg, plan_of(cfg, B, max_q, max_len, splits, 0), B, total_q);
     return KVQ_OK;
 }
 
@@ -788,7 +828,8 @@ int kvq_paged_attention(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, 
     if (!aligned16(q) || !aligned16(out) || (q_stride & 7)) return KVQ_ERR_ALIGN;
     if (q_stride < (int64_t)cfg->Hq * cfg->D) return KVQ_ERR_SHAPE;
     const Plan p = plan_of(cfg, B, max_q, max_len, splits, window);
-    const size_t need = ws_bytes(cfg, p, B);
+    if ((int64_t)p.S * p.nrb > INT32_MAX) return KVQ_ERR_RANGE;
+    const size_t need = ws_bytes(cfg, p, B, total_q);
     if (need > 0) {
         if (!workspace) return KVQ_ERR_NULL;
         if (!aligned16(workspace)) return KVQ_ERR_ALIGN;
@@ -804,17 +845,29 @@ int kvq_paged_attention(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, 
     a.out = (uint16_t*)out;
     a.lse = lse;
     a.part = (float*)workspace;
+    const size_t prow = p.nt ? (size_t)2 * p.S * 8 * p.nt : (size_t)p.S * total_q * cfg->Hq;
     if (p.join) {
-        a.pml = (float2*)(a.part + piece_rows(p) * cfg->D);
-        a.rec = (int4*)(a.pml + piece_rows(p));
-        a.by_request = p.nt && (int64_t)B * cfg->Hkv <= p.S;
+        a.pml = (float2*)(a.part + prow * cfg->D);
+        if (p.nt) {
+            a.rec = (int4*)(a.pml + prow);
+            a.by_request = (int64_t)B * cfg->Hkv <= p.S;
+        }
     }
     a.total_q = total_q, a.max_q = max_q, a.max_len = max_len, a.window = window, a.S = p.S;
     a.scale_log2 = (float)ldexp((double)sm_scale * 1.4426950408889634, cfg->k_exp);
     a.out_scale = ldexpf(1.0f, cfg->v_exp);
     const bool bf = cfg->dtype == KVQ_BF16;
     cudaStream_t st = (cudaStream_t)stream;
-    if (p.nt == 0) return run_chunk(a, B, p.nrb, st);
+    if (p.nt == 0) {
+        if ((e = run_chunk(a, p.nrb, B, st))) return e;
+        if (p.join) {
+            auto* mk = cfg->D == 64 ? (bf ? k_paged_merge<64, true> : k_paged_merge<64, false>)
+                                    : (bf ? k_paged_merge<128, true> : k_paged_merge<128, false>);
+            const int64_t R = (int64_t)max_q * (cfg->Hq / cfg->Hkv);
+            return launch_overlapped(mk, dim3((unsigned)((R + kMergeWarps - 1) / kMergeWarps), cfg->Hkv, B), kMergeWarps * 32, 0, 1, st, a);
+        }
+        return KVQ_OK;
+    }
     const int rows = max_q * (cfg->Hq / cfg->Hkv);
     if (cfg->D == 64)
         return p.nt == 1 ? (bf ? run_few<64, 1, true>(a, p, B, rows, st) : run_few<64, 1, false>(a, p, B, rows, st))

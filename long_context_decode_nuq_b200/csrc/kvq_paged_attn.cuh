@@ -19,8 +19,8 @@ struct AttnArgs {
     uint16_t* out;
     float *lse, *part;
     float2* pml;
-    int4* rec;        // what the join kernels have to join, or NULL
-    bool by_request;  // k_paged_join: a record per (request, kv head), else per block
+    int4* rec;        // few-row kernel: what k_paged_join has to join, or NULL
+    bool by_request;  // a record per (request, kv head), else per block
     int32_t total_q, max_q, max_len, window, S;
     float scale_log2, out_scale;
 };
@@ -48,8 +48,7 @@ __device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, f
 }  // namespace kvq
 
 namespace kvq_host {
-// Prompt chunks (kvq_paged_chunk.cu): query rows and tokens of a step, and the launch of a.S blocks
-// that share the steps, or (nrb > 0) take a row block each of the nrb that a request may have.
-constexpr int kChunkRows = 256, kChunkTokens = 128;
-int run_chunk(const kvq::AttnArgs& a, int B, int nrb, cudaStream_t stream);
+// Prompt chunks (kvq_paged_chunk.cu): query rows of a block, and the launch.
+constexpr int kChunkRows = 256;
+int run_chunk(const kvq::AttnArgs& a, int nrb, int B, cudaStream_t stream);
 }  // namespace kvq_host

@@ -7,13 +7,8 @@ using namespace kvq_host;
 namespace {
 
 // ---------------------------------------------------------------------------------
-// The work is a line of steps: 256 query rows of one (request, kv head) against 128 tokens, row
-// blocks and then kv heads of a request one after the other.  Block w of N takes steps
-// [w T / N, (w+1) T / N) of it, so all have the same share; rows whose steps one block has are
-// finished there, others leave (m, l, O) of each piece, at most two a block, for k_chunk_join.
-// Where that costs more than it evens out (a piece's O is 128 KB), a block takes a row block.
-//
-// In a step the rows are two tiles of 128.  Tensor memory holds, per tile, the scores S [128 x
+// A block takes 256 query rows of one (request, kv head), as two tiles of 128, and one split of
+// the tokens they see, 128 tokens at a time.  Tensor memory holds, per tile, the scores S [128 x
 // 128] and O [128 x D] in binary32; P overwrites S as fp16 and is the second product's operand
 // from there.  Roles, by warp:
 //   0-3, 4-7   softmax of a row tile, a thread a row: scores out of tensor memory, maximum, e^x,
@@ -45,13 +40,9 @@ struct Smem {
     static constexpr int raw = slot + kSlots * slot_bytes;   // [kRaw][8 groups]: keys or values
     static constexpr int raw_bytes = kTok / kGroup * Paged<D>::kHalf;
     static constexpr int bar = raw + kRaw * raw_bytes;
-    static constexpr int n_bar = 2 * kRaw + 2 * kSlots + 10;
+    static constexpr int n_bar = 2 * kRaw + 2 * kSlots + 8;
     static constexpr int misc = bar + 8 * n_bar;             // tmem address, dead flag, group masks
-    static constexpr int step = misc + 16;                   // int2 [8]: first token and length, of the last 8 steps
-    static constexpr int piece = step + 64;                  // int2 [2]: steps and row tiles of a piece, for the products
-    static constexpr int start = piece + 16;                 // where the block begins; sums of 16 warps
-    static constexpr int line = start + 48 + 16 * 8;         // Line [8], of the softmax warps
-    static constexpr int total = line + 8 * 128;
+    static constexpr int total = misc + 64;
 };
 
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* dead) {
@@ -155,75 +146,8 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) 
           "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
-// 256 rows of a (request, kv head) and the tokens they see.
-struct RowBlock {
-    int r0, rows, first;  // first: the position of the request's query 0
-    int lo, hi;           // tokens some row sees
-    int all_lo, all_hi;   // tokens every row sees
-    int tbase, n, u;      // steps, and units of the line: one where there is no step, to write zeros
-};
-__device__ __forceinline__ RowBlock row_block(const AttnArgs& a, const Rows& rw, int rb) {
-    const int G = a.c.Hq / a.c.Hkv;
-    RowBlock k;
-    k.r0 = rb * kRows;
-    k.rows = min(kRows, rw.R - k.r0);
-    const int i0 = k.r0 / G, i1 = (k.r0 + k.rows - 1) / G;
-    k.first = rw.len - rw.n;
-    k.hi = min(rw.kv, k.first + i1 + 1);
-    k.lo = a.window > 0 ? max(0, k.first + i0 + 1 - a.window) : 0;
-    k.all_hi = min(rw.kv, k.first + i0 + 1);
-    k.all_lo = a.window > 0 ? max(0, k.first + i1 + 1 - a.window) : 0;
-    k.tbase = k.lo & ~(kGroup - 1);
-    k.n = k.hi > k.lo ? (k.hi - k.tbase + kTok - 1) / kTok : 0;
-    k.u = max(k.n, 1);
-    return k;
-}
-// Units of one kv head of request b, summed by the warp's lanes.
-__device__ __forceinline__ int64_t request_units(const AttnArgs& a, const Rows& rw, int lane) {
-    int64_t sum = 0;
-    for (int rb = lane; rb * kRows < rw.R; rb += 32) sum += row_block(a, rw, rb).u;
-#pragma unroll
-    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    return sum;
-}
-
-// A walk over the pieces of a block's share of the line: the loader's own, and one in shared memory
-// for each softmax warp, whose registers are full.  The other warps are told by these.
-struct Line {
-    int64_t at, end;  // units still to take
-    int b, h, rb, u0; // of the next piece
-    Rows rw;
-    RowBlock k;
-    int un, tok0, n;  // of the present piece: units, first token, steps
-    bool whole, begins;
-};
-__device__ __forceinline__ bool next_piece(const AttnArgs& a, Line& p) {
-    if (p.at >= p.end) return false;
-    for (;;) {  // to a row block that has units left
-        if (p.rb * kRows < p.rw.R) {
-            p.k = row_block(a, p.rw, p.rb);
-            if (p.u0 < p.k.u) break;
-            ++p.rb;
-        } else if (p.rw.R > 0 && p.h + 1 < a.c.Hkv) {
-            p.rb = 0, ++p.h;
-        } else {
-            p.rb = p.h = 0;
-            p.rw = rows_of(a, ++p.b);
-        }
-        p.u0 = 0;
-    }
-    p.un = (int)min((int64_t)(p.k.u - p.u0), p.end - p.at);
-    p.begins = p.u0 == 0;
-    p.whole = p.un == p.k.u;
-    p.tok0 = p.k.tbase + p.u0 * kTok;
-    p.n = p.k.n == 0 ? 0 : p.un;
-    p.at += p.un;
-    p.u0 += p.un;
-    return true;
-}
-
 template <int D, bool BF>
-__global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, int B, int nrb) {
+__global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, int nrb) {
     using L = Smem<D>;
     constexpr int GPT = kTok / kGroup;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -234,18 +158,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
     uint64_t* s_full = kv_empty + kSlots;  // [2]
     uint64_t* p_full = s_full + 2;         // [2][2]: P's first and second 64 columns
     uint64_t* pv_done = p_full + 4;        // [2]
-    uint64_t* q_full = pv_done + 2;        // [2]
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + L::misc);
     volatile int* dead = reinterpret_cast<volatile int*>(smem + L::misc + 4);
-    uint8_t* gmask = smem + L::misc + 8;   // [8] groups that were brought, of the last 8 steps
-    int2* s_step = reinterpret_cast<int2*>(smem + L::step);
-    int2* s_piece = reinterpret_cast<int2*>(smem + L::piece);
-    static_assert(sizeof(Line) <= 128, "room for the softmax warps' lines");
-    int64_t* s_start = reinterpret_cast<int64_t*>(smem + L::start);
-    int64_t* s_sum = s_start + 6;
+    uint8_t* gmask = smem + L::misc + 8;   // [8] groups that were brought, of the last 8 tiles
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int s = blockIdx.x % a.S, rb = nrb - 1 - blockIdx.x / a.S, h = blockIdx.y, b = blockIdx.z;
     const int G = a.c.Hq / a.c.Hkv, P = a.c.page_tokens;
+    let_next();
+    after_previous();
+    const Rows rw = rows_of(a, b);
+    const int r0 = rb * kRows;
+    if (threadIdx.x == 0 && h == 0 && blockIdx.x == 0 && (rw.n > rw.nq || rw.len > rw.kv))
+        set_status(a.status, KVQ_STATUS_LEN_OVERFLOW);
+    if (r0 >= rw.R) return;
+    const int rows = min(kRows, rw.R - r0), nact = rows > 128 ? 2 : 1;
+    const int i0 = r0 / G, i1 = (r0 + rows - 1) / G;
+    const int first = rw.len - rw.n;
+    const int hi = min(rw.kv, first + i1 + 1);
+    const int lo = a.window > 0 ? max(0, first + i0 + 1 - a.window) : 0;
+    const int all_hi = min(rw.kv, first + i0 + 1);
+    const int all_lo = a.window > 0 ? max(0, first + i1 + 1 - a.window) : 0;
+    const int tbase = lo & ~(kGroup - 1);
+    const int tiles = hi > lo ? (hi - tbase + kTok - 1) / kTok : 0;
+    const int tb = (int)((int64_t)tiles * s / a.S);
+    const int n = (int)((int64_t)tiles * (s + 1) / a.S) - tb;  // steps of this block
+    const int tok0 = tbase + tb * kTok;
+
     if (warp == 13) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_at)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -254,157 +193,69 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
         *dead = 0;
         for (int i = 0; i < kRaw; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 4);
         for (int i = 0; i < kSlots; ++i) mbar_init(&kv_full[i], 4), mbar_init(&kv_empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&pv_done[i], 1), mbar_init(&q_full[i], 4);
+        for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&pv_done[i], 1);
         for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 4);
         fence_mbar_init();
     }
-    let_next();
-    after_previous();
-    // the block's share: a warp sums a run of requests, and the warp in whose run the share begins
-    // looks for the place
-    if (nrb == 0) {
-        const int per = (B + 15) / 16, b0 = min(B, warp * per), b1 = min(B, b0 + per);
-        int64_t mine = 0;
-        for (int b = b0; b < b1; ++b) {
-            const Rows rw = rows_of(a, b);
-            if (blockIdx.x == 0 && lane == 0 && (rw.n > rw.nq || rw.len > rw.kv)) set_status(a.status, KVQ_STATUS_LEN_OVERFLOW);
-            mine += request_units(a, rw, lane);
-        }
-        if (lane == 0) s_sum[warp] = mine;
-        __syncthreads();
-        int64_t before = 0, total = 0;
-        for (int w = 0; w < 16; ++w) {
-            if (w < warp) before += s_sum[w];
-            total += s_sum[w];
-        }
-        const int64_t T = total * a.c.Hkv, N = min((int64_t)gridDim.x, T);
-        if (threadIdx.x == 0) s_start[0] = T, s_start[1] = N;
-        const int64_t g0 = N ? T * blockIdx.x / N : 0;
-        if ((int64_t)blockIdx.x < N && before * a.c.Hkv <= g0 && g0 < (before + mine) * a.c.Hkv) {
-            int b = b0;
-            for (;; ++b) {
-                const Rows rw = rows_of(a, b);
-                const int64_t u = request_units(a, rw, lane);
-                if ((before + u) * a.c.Hkv > g0) {
-                    int64_t off = g0 - before * a.c.Hkv;
-                    const int h = (int)(off / u);
-                    off -= h * u;
-                    int rb = 0, ub = 0;  // 32 row blocks at a time
-                    for (;; rb += 32) {
-                        int64_t incl = (rb + lane) * kRows < rw.R ? row_block(a, rw, rb + lane).u : 0;
-                        const int uu = (int)incl;
-#pragma unroll
-                        for (int x = 1; x < 32; x <<= 1) {
-                            const int64_t y = __shfl_up_sync(0xffffffffu, incl, x);
-                            if (lane >= x) incl += y;
-                        }
-                        const uint32_t past = __ballot_sync(0xffffffffu, incl > off);
-                        if (past) {
-                            const int z = __ffs(past) - 1;
-                            ub = (int)(off - __shfl_sync(0xffffffffu, incl - uu, z));
-                            rb += z;
-                            break;
-                        }
-                        off -= __shfl_sync(0xffffffffu, incl, 31);
-                    }
-                    if (lane == 0) s_start[2] = b, s_start[3] = h, s_start[4] = rb, s_start[5] = ub;
-                    break;
-                }
-                before += u;
+    // queries: a thread a row, its power of two kept for the scores
+    const int row = threadIdx.x;  // of the block, for warps 0-7
+    const int r = r0 + row;
+    float sl2 = 0.0f;
+    if (warp < 8) {
+        const bool real = r < rw.R;
+        const uint16_t* src = a.q + (int64_t)(rw.c0 + (real ? r / G : 0)) * a.qs + (h * G + (real ? r % G : 0)) * D;
+        int e = 0;
+        if (BF && real) {
+            uint32_t mx = 0;
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 x = reinterpret_cast<const uint4*>(src)[i];
+                mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
             }
+            const int eb = (int)(max(mx & 0xffffu, mx >> 16) >> 7);
+            if (eb < 255) e = max(eb - 127 - 10, -120);
         }
+        // a negative scale goes into the query, so that the largest score is the largest product
+        const float f = __uint_as_float((uint32_t)(127 - e) << 23) * (a.scale_log2 < 0.0f ? -1.0f : 1.0f);
+        sl2 = fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + e) << 23), 1e-37f);
+        for (int i = 0; i < D / 8; ++i) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (real) x = reinterpret_cast<const uint4*>(src)[i];
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z) w[z] = pack_h2(lo16<BF>(w[z]) * f, hi16<BF>(w[z]) * f);
+            *reinterpret_cast<uint4*>(smem + L::q + (i / 8) * (kRows * 128) + row * 128 + ((i % 8 ^ (row & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async();
     }
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = *tmem_at;
-    const int64_t T = nrb ? 0 : s_start[0], N = nrb ? 0 : s_start[1];
-    const int64_t g0 = N ? T * blockIdx.x / N : 0;
-    auto begin = [&] {
-        Line p{};
-        if (nrb) {  // a block a row block, those that see most first
-            p.rb = nrb - 1 - (int)(blockIdx.x % nrb), p.h = (int)(blockIdx.x / nrb % a.c.Hkv), p.b = (int)(blockIdx.x / nrb / a.c.Hkv);
-            p.rw = rows_of(a, p.b);
-            if (p.rb * kRows < p.rw.R) p.end = row_block(a, p.rw, p.rb).u;
-            if (threadIdx.x == 0 && p.h == 0 && p.rb == 0 && (p.rw.n > p.rw.nq || p.rw.len > p.rw.kv))
-                set_status(a.status, KVQ_STATUS_LEN_OVERFLOW);
-        } else if ((int64_t)blockIdx.x < N) {
-            p.at = g0, p.end = T * (blockIdx.x + 1) / N;
-            p.b = (int)s_start[2], p.h = (int)s_start[3], p.rb = (int)s_start[4], p.u0 = (int)s_start[5];
-            p.rw = rows_of(a, p.b);
-        }
-        return p;
-    };
 
+    float m = -INFINITY, l = 0.0f;
     if (warp < 8) {
         regs_up<kRegSoft>();
-        const int i = warp >> 2, row = threadIdx.x;  // tile, and row of the 256
+        const int i = warp >> 2;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, in bits 16 and up
         const uint32_t st = tmem + lanes + i * 128, ot = tmem + lanes + 256 + i * D;
-        int done = 0, mine = 0, ended = 0;  // steps of the block, steps and pieces of this tile
-        Line& line = reinterpret_cast<Line*>(smem + L::line)[warp];
-        if (lane == 0) line = begin();
-        for (;;) {
-            const bool more = __shfl_sync(0xffffffffu, lane == 0 && !*dead && next_piece(a, line), 0);
-            if (!more) break;
-            __syncwarp();  // lane 0's writes
-            const Rows& rw = line.rw;
-            const RowBlock& k = line.k;
-            const int n = line.n, nact = k.rows > 128 ? 2 : 1, r = k.r0 + row, h = line.h;
-            const bool real = row < k.rows;
-            float sl2 = 0.0f, m = -INFINITY, l = 0.0f;
-            if (i < nact && n > 0) {
-                // queries, a thread a row, its power of two kept for the scores.  The products
-                // that read the rows before are complete: this tile's last scores were awaited
-                const uint16_t* src = a.q + (int64_t)(rw.c0 + (real ? r / G : 0)) * a.qs + (h * G + (real ? r % G : 0)) * D;
-                int e = 0;
-                if (BF && real) {
-                    uint32_t mx = 0;
-#pragma unroll 4
-                    for (int z = 0; z < D / 8; ++z) {
-                        const uint4 x = reinterpret_cast<const uint4*>(src)[z];
-                        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-                    }
-                    const int eb = (int)(max(mx & 0xffffu, mx >> 16) >> 7);
-                    if (eb < 255) e = max(eb - 127 - 10, -120);
-                }
-                // a negative scale goes into the query, so that the largest score is the
-                // largest product
-                const float f = __uint_as_float((uint32_t)(127 - e) << 23) * (a.scale_log2 < 0.0f ? -1.0f : 1.0f);
-                sl2 = fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + e) << 23), 1e-37f);
-#pragma unroll 4
-                for (int z = 0; z < D / 8; ++z) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (real) x = reinterpret_cast<const uint4*>(src)[z];
-                    uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) w[y] = pack_h2(lo16<BF>(w[y]) * f, hi16<BF>(w[y]) * f);
-                    *reinterpret_cast<uint4*>(smem + L::q + (z / 8) * (kRows * 128) + row * 128 + ((z % 8 ^ (row & 7)) << 4)) =
-                        make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                fence_proxy_async();
-                if (threadIdx.x == 0) s_piece[ended & 1] = make_int2(n, nact);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&q_full[i]);
-            }
-            const int pos = k.first + r / G;
-            const int hi_r = min(rw.kv, pos + 1), lo_r = a.window > 0 ? pos + 1 - a.window : 0;
-            const int all_hi = k.all_hi, all_lo = k.all_lo, tok0 = line.tok0;
-            if (i < nact)
+        const int pos = first + r / G;
+        const int hi_r = min(rw.kv, pos + 1), lo_r = a.window > 0 ? pos + 1 - a.window : 0;
+        if (i < nact)
             for (int j = 0; j < n; ++j) {
-                if (!__all_sync(0xffffffffu, wait_on(&s_full[i], (mine + j) & 1, dead))) break;
+                if (!__all_sync(0xffffffffu, wait_on(&s_full[i], j & 1, dead))) break;
                 fence_after();
                 // these scores are complete, and with them all that was issued before: K_j's slot
                 // and V_(j-1)'s are free
                 if (i == nact - 1 && (threadIdx.x & 127) == 0) {
-                    mbar_arrive(&kv_empty[2 * (done + j) % kSlots]);
-                    if (j > 0) mbar_arrive(&kv_empty[(2 * (done + j) - 1) % kSlots]);
+                    mbar_arrive(&kv_empty[2 * j % kSlots]);
+                    if (j > 0) mbar_arrive(&kv_empty[(2 * j - 1) % kSlots]);
                 }
                 uint32_t x[2][64];
                 tmem_ld64(x[0], st);
                 tmem_ld64(x[1], st + 64);
                 const int t0 = tok0 + j * kTok;
-                const uint32_t got = gmask[(done + j) & 7];
+                const uint32_t got = gmask[j & 7];
                 if (got != 0xffu || t0 + kTok > all_hi || t0 < all_lo) {
 #pragma unroll
                     for (int c = 0; c < kTok; ++c) {
@@ -461,78 +312,60 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
                 const f2 u = upk(sum[0]), v = upk(sum[1]);
                 l += (u.x + u.y) + (v.x + v.y);
             }
-            // the row's output
-            if (i < nact && n > 0) {
-                __all_sync(0xffffffffu, wait_on(&pv_done[i], ended & 1, dead));
-                fence_after();
-                if (i == nact - 1 && (threadIdx.x & 127) == 0) mbar_arrive(&kv_empty[(2 * (done + n) - 1) % kSlots]);
-                mine += n;
-                ++ended;
+        // the row's output
+        if (i < nact && n > 0) {
+            __all_sync(0xffffffffu, wait_on(&pv_done[i], 0, dead));
+            fence_after();
+        }
+        const bool real = i < nact && r < rw.R;
+        const int64_t nrow = (int64_t)a.total_q * a.c.Hq;
+        const int64_t grow = (int64_t)(rw.c0 + r / G) * a.c.Hq + h * G + r % G;
+        const float inv = l == 0.0f ? 0.0f : a.out_scale / l;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            if (n > 0 && i < nact) {
+                tmem_ld32(o, ot + c);
+            } else {
+#pragma unroll
+                for (int z = 0; z < 32; ++z) o[z] = 0u;
             }
-            const int64_t grow = (int64_t)(rw.c0 + r / G) * a.c.Hq + h * G + r % G;
-            const int64_t prow = (2 * (int64_t)blockIdx.x + (line.at - line.un != g0)) * kRows + row;
-            const float inv = l == 0.0f ? 0.0f : a.out_scale / l;
+            // a row that saw nothing has P = 0 times finite values: O = 0 exactly
+            if (!real) continue;
+            if (a.S == 1) {
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                __syncwarp();
-                if (n > 0 && i < nact) {
-                    tmem_ld32(o, ot + c);
-                } else {
+                for (int z = 0; z < 32; z += 8) {
+                    uint32_t w[4];
 #pragma unroll
-                    for (int z = 0; z < 32; ++z) o[z] = 0u;
+                    for (int y = 0; y < 4; ++y)
+                        w[y] = pack16<BF>(__uint_as_float(o[z + 2 * y]) * inv, __uint_as_float(o[z + 2 * y + 1]) * inv);
+                    *reinterpret_cast<uint4*>(a.out + grow * D + c + z) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                // a row that saw nothing has P = 0 times finite values: O = 0 exactly
-                if (!real) continue;
-                if (line.whole) {
+            } else {
 #pragma unroll
-                    for (int z = 0; z < 32; z += 8) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            w[y] = pack16<BF>(__uint_as_float(o[z + 2 * y]) * inv, __uint_as_float(o[z + 2 * y + 1]) * inv);
-                        *reinterpret_cast<uint4*>(a.out + grow * D + c + z) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                } else {
-#pragma unroll
-                    for (int z = 0; z < 32; z += 4)
-                        *reinterpret_cast<uint4*>(a.part + prow * D + c + z) = make_uint4(o[z], o[z + 1], o[z + 2], o[z + 3]);
-                }
-            }
-            if (real) {
-                if (!line.whole) a.pml[prow] = make_float2(m, l);
-                else if (a.lse) a.lse[grow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
-            }
-            fence_before();
-            done += n;
-            __syncwarp();  // before lane 0 moves the line on
-            // the first piece of rows that others continue says where all pieces are
-            if (threadIdx.x == 0 && a.rec && line.begins && !line.whole) {
-                const int64_t end = line.at - line.un + k.u;
-                a.rec[2 * blockIdx.x] = make_int4((int)((end * N - 1) / T), (int)(prow / kRows), k.rows, h);
-                a.rec[2 * blockIdx.x + 1] = make_int4(rw.c0, k.r0, 0, 0);
+                for (int z = 0; z < 32; z += 4)
+                    *reinterpret_cast<uint4*>(a.part + (s * nrow + grow) * D + c + z) = make_uint4(o[z], o[z + 1], o[z + 2], o[z + 3]);
             }
         }
-        if (i == 0) {  // no more pieces
-            if (threadIdx.x == 0) s_piece[ended & 1] = make_int2(0, 0);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full[0]);
+        if (real) {
+            if (a.S > 1) a.pml[s * nrow + grow] = make_float2(m, l);
+            else if (a.lse) a.lse[grow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
-        // only a block's last piece can be one
-        if (threadIdx.x == 0 && a.rec && !(line.un > 0 && line.begins && !line.whole)) a.rec[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+        fence_before();
     } else if (warp < 12) {
         regs_down<kRegDeq>();
         const int tid = threadIdx.x - 256;
         constexpr int LPR = D / 32;          // lanes of a token's row, 16 code bytes each
         constexpr int RPP = 128 / LPR;       // rows a pass
         const int q = tid % LPR, rr = tid / LPR;
-        for (int seq = 0;; ++seq) {  // K_0, V_0, K_1, ...
+        for (int seq = 0; seq < 2 * n; ++seq) {  // K_0, V_0, K_1, ...
             const int rs = seq % kRaw, slot = seq % kSlots, j = seq >> 1;
             const bool val = seq & 1;
-            if (!__all_sync(0xffffffffu, wait_on(&raw_full[rs], (seq / kRaw) & 1, dead))) break;
-            const int t0 = s_step[j & 7].x, kv = s_step[j & 7].y;
-            if (kv < 0 || !__all_sync(0xffffffffu, wait_on(&kv_empty[slot], (seq / kSlots + 1) & 1, dead))) break;
+            if (!__all_sync(0xffffffffu, wait_on(&raw_full[rs], (seq / kRaw) & 1, dead) &&
+                                             wait_on(&kv_empty[slot], (seq / kSlots + 1) & 1, dead)))
+                break;
             const uint32_t got = gmask[j & 7];
+            const int t0 = tok0 + j * kTok;
             uint8_t* dst = smem + L::slot + slot * L::slot_bytes + (q >> 1) * (kTok * 128);
             const uint8_t* src = smem + L::raw + rs * L::raw_bytes;
 #pragma unroll
@@ -542,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
                 const uint4 c4 = *reinterpret_cast<const uint4*>(g + (t % kGroup) * Paged<D>::kRow + q * 16);
                 uint32_t sc = *reinterpret_cast<const uint16_t*>(g + kGroup * Paged<D>::kRow + (t % kGroup) * Paged<D>::kScales + q * 2);
                 // bytes nobody wrote may hold NaN scales; as values they must be 0
-                if (val && (t0 + t >= kv || !(got >> (t / kGroup) & 1u))) sc = 0;
+                if (val && (t0 + t >= rw.kv || !(got >> (t / kGroup) & 1u))) sc = 0;
                 const uint32_t two = e4m3x2(sc);
                 const uint32_t s2[2] = {__byte_perm(two, 0, 0x1010), __byte_perm(two, 0, 0x3232)};
                 const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
@@ -570,41 +403,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
     } else {
         regs_down<kRegIssue>();
         if (warp == 12) {
-            int seq = 0;
-            Line line = begin();
-            while (!*dead && next_piece(a, line)) {
-                const int32_t* tab = a.table + (size_t)line.b * a.c.max_pages;
-                const int n = line.n, s0 = seq, hi = line.k.hi, lo = line.k.lo, t0 = line.tok0 + lane * kGroup;
-                auto wanted = [&](int j) {
-                    const int tg = t0 + j * kTok;
-                    return lane < GPT && j < n && tg < hi && tg + kGroup > lo;
-                };
-                auto page_of = [&](int j) { return wanted(j) ? tab[(t0 + j * kTok) / P] : -1; };
-                int page = page_of(0), next = page_of(1);
-                for (; seq < s0 + 2 * n; ++seq) {
-                    const int rs = seq % kRaw, j = (seq - s0) >> 1;
-                    if (!__all_sync(0xffffffffu, wait_on(&raw_empty[rs], (seq / kRaw + 1) & 1, dead))) break;
-                    const int tg = t0 + j * kTok;
-                    const bool want = wanted(j), ok = want && page >= 0 && page < a.c.num_pages;
-                    if (want && !ok) set_status(a.status, KVQ_STATUS_BAD_PAGE);
-                    const uint32_t v = __ballot_sync(0xffffffffu, ok);
-                    if (lane == 0) {
-                        gmask[(seq >> 1) & 7] = (uint8_t)v;
-                        s_step[(seq >> 1) & 7] = make_int2(line.tok0 + j * kTok, line.rw.kv);
-                        mbar_arrive_expect_tx(&raw_full[rs], __popc(v) * Paged<D>::kHalf);
-                    }
-                    __syncwarp();
-                    if (ok)
-                        bulk_load(smem + L::raw + rs * L::raw_bytes + lane * Paged<D>::kHalf,
-                                  a.pool + group_at(a.c, page, line.h, tg % P / kGroup) + (seq & 1) * Paged<D>::kHalf,
-                                  Paged<D>::kHalf, &raw_full[rs]);
-                    if (seq & 1) page = next, next = page_of(j + 2);
+            const int32_t* tab = a.table + (size_t)b * a.c.max_pages;
+            auto wanted = [&](int j) {
+                const int tg = tok0 + j * kTok + lane * kGroup;
+                return lane < GPT && j < n && tg < hi && tg + kGroup > lo;
+            };
+            auto page_of = [&](int j) { return wanted(j) ? tab[(tok0 + j * kTok + lane * kGroup) / P] : -1; };
+            int page = page_of(0), next = page_of(1), seq = 0;
+            for (; seq < 2 * n; ++seq) {
+                const int rs = seq % kRaw, j = seq >> 1;
+                if (!__all_sync(0xffffffffu, wait_on(&raw_empty[rs], (seq / kRaw + 1) & 1, dead))) break;
+                const int tg = tok0 + j * kTok + lane * kGroup;
+                const bool want = wanted(j), ok = want && page >= 0 && page < a.c.num_pages;
+                if (want && !ok) set_status(a.status, KVQ_STATUS_BAD_PAGE);
+                const uint32_t v = __ballot_sync(0xffffffffu, ok);
+                if (lane == 0) {
+                    gmask[j & 7] = (uint8_t)v;
+                    mbar_arrive_expect_tx(&raw_full[rs], __popc(v) * Paged<D>::kHalf);
                 }
-            }
-            // no more steps
-            if (__all_sync(0xffffffffu, wait_on(&raw_empty[seq % kRaw], (seq / kRaw + 1) & 1, dead)) && lane == 0) {
-                s_step[(seq >> 1) & 7] = make_int2(0, -1);
-                mbar_arrive(&raw_full[seq % kRaw]);
+                __syncwarp();
+                if (ok)
+                    bulk_load(smem + L::raw + rs * L::raw_bytes + lane * Paged<D>::kHalf,
+                              a.pool + group_at(a.c, page, h, tg % P / kGroup) + (seq & 1) * Paged<D>::kHalf,
+                              Paged<D>::kHalf, &raw_full[rs]);
+                if (seq & 1) page = next, next = page_of(j + 2);
             }
             if (*dead)  // let the copies in flight land before the memory is left
                 for (int k = max(0, seq - kRaw); k < seq; ++k) mbar_wait(&raw_full[k % kRaw], (k / kRaw) & 1);
@@ -628,41 +450,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
                 for (int k = 4 * half; k < 4 * half + 4; ++k)
                     mma_ts(tmem + 256 + i * D, tmem + i * 128 + k * 8, vi + k * (2048 / 16), io, add || k > 0);
             };
-            bool ok = true;
-            int seq = 0, pieces[2] = {0, 0}, steps[2] = {0, 0};  // K's place in the ring; pieces and steps of a tile
-            while (ok) {
-                // the queries of the next piece, and what it is
-                ok = wait_on(&q_full[0], pieces[0] & 1, dead);
-                const int n = s_piece[pieces[0] & 1].x, nact = s_piece[pieces[0] & 1].y;
-                if (!ok || n == 0) break;
-                ++pieces[0];
-                if (nact > 1) ok = wait_on(&q_full[1], pieces[1]++ & 1, dead);
-                ok = ok && wait_on(&kv_full[seq % kSlots], (seq / kSlots) & 1, dead);
-                if (!ok) break;
+            bool ok = n > 0 && wait_on(&kv_full[0], 0, dead);
+            if (ok) {
                 fence_after();
-                for (int i = 0; i < nact; ++i) scores(i, seq % kSlots);
-                for (int j = 0; j < n && ok; ++j, seq += 2) {
-                    const int vs = seq + 1, ks = seq + 2;
-                    ok = wait_on(&kv_full[vs % kSlots], (vs / kSlots) & 1, dead);
-                    for (int i = 0; i < nact && ok; ++i) {
-                        for (int half = 0; half < 2 && ok; ++half) {
-                            ok = wait_on(&p_full[2 * i + half], (steps[i] + j) & 1, dead);
+                for (int i = 0; i < nact; ++i) scores(i, 0);
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                const int vs = 2 * j + 1, ks = 2 * j + 2;
+                ok = wait_on(&kv_full[vs % kSlots], (vs / kSlots) & 1, dead);
+                for (int i = 0; i < nact && ok; ++i) {
+                    for (int half = 0; half < 2 && ok; ++half) {
+                        ok = wait_on(&p_full[2 * i + half], j & 1, dead);
+                        fence_after();
+                        if (ok) values(i, vs % kSlots, half, j > 0);
+                    }
+                    if (j + 1 == n) {
+                        mma_commit(&pv_done[i]);
+                    } else if (ok) {
+                        if (i == 0) {
+                            ok = wait_on(&kv_full[ks % kSlots], (ks / kSlots) & 1, dead);
                             fence_after();
-                            if (ok) values(i, vs % kSlots, half, j > 0);
+                            if (!ok) break;
                         }
-                        if (j + 1 == n) {
-                            mma_commit(&pv_done[i]);
-                        } else if (ok) {
-                            if (i == 0) {
-                                ok = wait_on(&kv_full[ks % kSlots], (ks / kSlots) & 1, dead);
-                                fence_after();
-                                if (!ok) break;
-                            }
-                            scores(i, ks % kSlots);
-                        }
+                        scores(i, ks % kSlots);
                     }
                 }
-                for (int i = 0; i < nact; ++i) steps[i] += n;
             }
             if (*dead) {  // products in flight end before the memory is given back
                 mma_commit(&s_full[0]);
@@ -679,44 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
     }
 }
 
-// Joins what block boundaries cut: block (x, y) takes rows [8 y, 8 y + 8) of record x, a warp a row,
-// and adds its pieces in order of their blocks.
-constexpr int kJoinRows = 8;
 template <int D, bool BF>
-__global__ void __launch_bounds__(kJoinRows * 32) k_chunk_join(const AttnArgs a) {
-    const int lane = threadIdx.x & 31, row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
-    let_next();
-    after_previous();
-    const int4 rec = a.rec[2 * blockIdx.x], who = a.rec[2 * blockIdx.x + 1];
-    const int w1 = rec.x, w0 = rec.y >> 1;
-    if (w1 < 0 || row >= rec.z) return;
-    constexpr int V = D / 32;
-    float acc[V] = {}, M = -INFINITY, L = 0.0f;
-    for (int w = w0; w <= w1; ++w) {
-        const int64_t at = (w == w0 ? (int64_t)rec.y : 2 * (int64_t)w) * kRows + row;
-        const float2 ml = a.pml[at];
-        float x[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = a.part[at * D + lane * V + i];
-        const float mn = fmaxf(M, ml.x);
-        // l = 0: saw nothing, m = -inf; a row of NaN scores has m = -inf, l = NaN
-        const float f = L == 0.0f ? 0.0f : ex2(M - mn), e = ml.y == 0.0f ? 0.0f : ex2(ml.x - mn);
-        L = L * f + e * ml.y;
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = acc[i] * f + e * x[i];
-        M = mn;
-    }
-    const int G = a.c.Hq / a.c.Hkv, r = who.y + row;
-    const int64_t grow = (int64_t)(who.x + r / G) * a.c.Hq + rec.w * G + r % G;
-    const float inv = L == 0.0f ? 0.0f : a.out_scale / L;
-#pragma unroll
-    for (int i = 0; i < V; i += 2)
-        reinterpret_cast<uint32_t*>(a.out + grow * D + lane * V)[i / 2] = pack16<BF>(acc[i] * inv, acc[i + 1] * inv);
-    if (lane == 0 && a.lse) a.lse[grow] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
-}
-
-template <int D, bool BF>
-int launch(const AttnArgs& a, int B, int nrb, cudaStream_t st) {
+int launch(const AttnArgs& a, int nrb, int B, cudaStream_t st) {
     auto* kern = k_paged_chunk<D, BF>;
     constexpr int smem = Smem<D>::total;
     static_assert(smem <= 232448, "shared memory of a block");
@@ -728,17 +504,15 @@ int launch(const AttnArgs& a, int B, int nrb, cudaStream_t st) {
         return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
     }();
     if (regs * 4 < 2 * kRegSoft + kRegDeq + kRegIssue) return KVQ_ERR_UNSUPPORTED;
-    const int e = launch_overlapped(kern, dim3(a.S), kThreads, smem, 1, st, a, B, nrb);
-    if (e || !a.rec) return e;
-    return launch_overlapped(k_chunk_join<D, BF>, dim3(a.S, kRows / kJoinRows), kJoinRows * 32, 0, 1, st, a);
+    return launch_overlapped(kern, dim3((unsigned)(a.S * nrb), a.c.Hkv, B), kThreads, smem, 1, st, a, nrb);
 }
 
 }  // namespace
 
 namespace kvq_host {
-int run_chunk(const AttnArgs& a, int B, int nrb, cudaStream_t st) {
+int run_chunk(const AttnArgs& a, int nrb, int B, cudaStream_t st) {
     const bool bf = a.c.dtype == KVQ_BF16;
-    if (a.c.D == 64) return bf ? launch<64, true>(a, B, nrb, st) : launch<64, false>(a, B, nrb, st);
-    return bf ? launch<128, true>(a, B, nrb, st) : launch<128, false>(a, B, nrb, st);
+    if (a.c.D == 64) return bf ? launch<64, true>(a, nrb, B, st) : launch<64, false>(a, nrb, B, st);
+    return bf ? launch<128, true>(a, nrb, B, st) : launch<128, false>(a, nrb, B, st);
 }
 }  // namespace kvq_host

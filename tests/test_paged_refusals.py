@@ -89,9 +89,9 @@ def test_workspace_sizes():
     # 16 rows a kv head: pieces of two per block, and a count per request
     n = [K.kvq_paged_attention_workspace(cfg(), 3, 9, 4, 5000, s) for s in (0, 1, 2, 256)]
     assert n[1] == 2 * 6 * 16 * 130 * 4 + 6 * 16 and n[1] < n[2] < n[0] < n[3]
-    # 800 rows a kv head, 24 blocks of 256 rows: two pieces of them per block
-    n = [K.kvq_paged_attention_workspace(cfg(), 3, 600, 200, 5000, s) for s in (0, 1, 2)]
-    assert n == [b * (2 * 256 * 130 * 4 + 32) for b in (148, 0, 48)]
+    # 800 rows: splits of all rows
+    n = [K.kvq_paged_attention_workspace(cfg(), 3, 600, 200, 5000, s) for s in (1, 2, 256)]
+    assert n == [0, 2 * 600 * 8 * 130 * 4, 256 * 600 * 8 * 130 * 4]
     assert K.kvq_paged_attention_workspace(cfg(), 3, 3, 1, 64) == 0
 
 
