@@ -8,6 +8,7 @@ import torch
 
 import long_context_decode_nuq_b200 as K
 import paged_testlib as R
+from long_context_decode_nuq_b200.paged import PagedSession
 
 pytestmark = pytest.mark.gpu
 DT = {"fp16": torch.float16, "bf16": torch.bfloat16}
@@ -139,7 +140,7 @@ def run_plan(c, lens, n_new, table, free, n_free, capacity, in_place=False):
 @pytest.mark.parametrize("P", [16, 128])
 @pytest.mark.parametrize("B,T,n,width,spare,extra", [
     (1, 0, 1, 4, 5, 0), (1, 100, 0, 8, 0, 3), (5, 60, 9, 8, 50, 0), (33, 300, 40, 20, 7, 5), (33, 300, 40, 20, 7, -300),
-    (1024, 90, 3, 8, 4000, 0), (1025, 90, 5, 8, 300, 9), (3000, 500, 20, 40, 9000, 100), (2, 9000, 20000, 2000, 3000, 0)])
+    (1024, 90, 3, 8, 4000, 0), (1025, 90, 5, 8, 300, 9), (3000, 500, 20, 40, 9000, 100), (9001, 100, 6, 9, 20000, 3), (2, 9000, 20000, 2000, 3000, 0)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_plan(P, B, T, n, width, spare, extra, in_place):
     r = random.Random(B * 31 + P)
@@ -262,6 +263,14 @@ CASES = [
     ("bf16", 64, 64, 1, 3, [500, 77, 300], [9, 9, 130], 33, 0),
     ("bf16", 128, 64, 1, 4, [500, 77, 300], [200, 77, 130], 100, 3),
     ("fp16", 128, 16, 1, 1, [2000], [300], 10000, 0),
+    # long ones, by the library's choice: a line of units cut anywhere, several splits
+    ("bf16", 128, 64, 2, 4, [6000, 1, 900], [1, 1, 1], 0, 0),
+    ("fp16", 64, 32, 1, 2, [9000, 40, 0, 2500], [8, 8, 8, 5], 0, 0),
+    ("bf16", 64, 128, 1, 4, [4000, 130], [33, 20], 0, 0),
+    # more requests than lanes, and than threads of a block; empty ones among them
+    ("bf16", 128, 16, 1, 2, [(b * 37) % 190 for b in range(40)], [b % 3 for b in range(40)], 0, 0),
+    ("fp16", 64, 16, 2, 1, [(b * 37) % 190 for b in range(300)], [(b + 1) % 2 for b in range(300)], 0, 2),
+    ("bf16", 64, 16, 1, 6, [(b * 53) % 90 for b in range(300)], [b % 6 for b in range(300)], 0, 1),
 ]
 
 
@@ -367,91 +376,147 @@ def test_attention_reports_lengths_past_the_bounds(n):
     assert np.all(np.abs(f64(out) - want) <= np.abs(want) * 2.0 ** -8 + pv * 2.0 ** -10)
 
 
-def test_attention_nan_query_stays_in_its_row():
+@pytest.mark.parametrize("scale", [-0.07, 0.0, 30.0])
+@pytest.mark.parametrize("n", [1, 40])
+def test_attention_scales(scale, n):
+    for dtype in ("fp16", "bf16"):
+        c = make(dtype, 4, 1, 128, 16, 40, 40)
+        table, kv = fill(c, dtype, [333], 3)
+        q = rand((n, 4, 128), dtype, 4)
+        out, lse = torch.empty_like(q), torch.empty((n, 4), device="cuda")
+        ws = torch.empty(max(16, K.kvq_paged_attention_workspace(c.cfg, 1, n, n, 333)), dtype=torch.uint8, device="cuda")
+        K.kvq_paged_attention(c, q, i32([0, n]), i32([333]), table, n, 333, scale, out, ws, lse=lse)
+        check(out, lse, f64(q), kv, [n], scale, 0, dtype)
+
+
+@pytest.mark.parametrize("splits", [0, 2])
+def test_attention_nan_query_stays_in_its_row(splits):
     for n in (1, 6, 100):
         c = make("bf16", 4, 1, 128, 16, 30, 20)
         table, kv = fill(c, "bf16", [160], 3)
         q = rand((n, 4, 128), "bf16", 4)
         q[0, 2, 5] = float("nan")
         out = torch.empty_like(q)
-        ws = torch.empty(K.kvq_paged_attention_workspace(c.cfg, 1, n, n, 160), dtype=torch.uint8, device="cuda")
-        K.kvq_paged_attention(c, q, i32([0, n]), i32([160]), table, n, 160, 0.1, out, ws)
+        ws = torch.empty(max(16, K.kvq_paged_attention_workspace(c.cfg, 1, n, n, 160, splits)), dtype=torch.uint8, device="cuda")
+        K.kvq_paged_attention(c, q, i32([0, n]), i32([160]), table, n, 160, 0.1, out, ws, splits=splits)
         bad = torch.isnan(out).any(-1)
         assert bool(bad[0, 2]) and int(bad.sum()) == 1
 
 
 # ------------------------------------------------------------------------------ together
-def serve(c, steps, stream=None):
-    """Rounds of plan, rotate, append, attend over requests of changing lengths."""
-    cfg = c.cfg
-    B, P, D = 5, cfg.page_tokens, cfg.D
-    rope = K.make_rope_cfg(cfg.Hq, cfg.Hkv, D, D, [0] * (D // 2), c.dtype)
+def serve(cfg, steps, layers=2, finish=None):
+    """Rounds of a session over requests of changing lengths, every layer against 64 bits."""
+    B, D = len(steps[0]), cfg.D
+    rope = K.make_rope_cfg(cfg.Hq, cfg.Hkv, D, D, [0] * (D // 2), torch.bfloat16)
     freqs = 1e4 ** (-torch.arange(D // 2, dtype=torch.float64, device="cuda") / (D // 2))
-    free, n_free = i32(np.random.RandomState(1).permutation(cfg.num_pages)), i32([cfg.num_pages])
-    lens, table = i32([0] * B), i32(np.full((B, cfg.max_pages), -1))
-    hist = [([], []) for _ in range(B)]
+    s = PagedSession(cfg, layers, B, rope, freqs)
+    for c in s.caches:
+        c.pool.fill_(0xFF)
+    hist = [[([np.zeros((0, cfg.Hkv, D))], [np.zeros((0, cfg.Hkv, D))]) for _ in range(B)] for _ in range(layers)]
     for step, new in enumerate(steps):
         n = sum(new)
-        qkv = rand((n, cfg.Hq + 2 * cfg.Hkv, D), "bf16", 100 + step)
-        q, k, v = qkv[:, :cfg.Hq], qkv[:, cfg.Hq:cfg.Hq + cfg.Hkv], qkv[:, cfg.Hq + cfg.Hkv:]
-        cu = torch.empty(B + 1, dtype=torch.int32, device="cuda")
-        slots, pos = torch.empty(n, dtype=torch.int32, device="cuda"), torch.empty(n, dtype=torch.int32, device="cuda")
-        K.kvq_page_plan(c, lens, i32(new), table, free, n_free, cu, lens, n_free, slots, pos)
-        K.kvq_rope(rope, q, k, pos, freqs, q, k)  # in place, inside the projection
-        K.kvq_paged_append(c, k, v, slots)
-        out = torch.empty((n, cfg.Hq, D), dtype=c.dtype, device="cuda")
-        mq, ml = max(new), cfg.max_pages * P
-        ws = torch.empty(K.kvq_paged_attention_workspace(cfg, B, n, mq, ml), dtype=torch.uint8, device="cuda")
-        K.kvq_paged_attention(c, q, cu, lens, table, mq, ml, D ** -0.5, out, ws)
-        at = 0
-        for b, m in enumerate(new):
-            hist[b][0].append(R.quantize(f64(k[at:at + m])))
-            hist[b][1].append(R.quantize(f64(v[at:at + m])))
-            at += m
-        kv = [(np.concatenate(a), np.concatenate(z)) for a, z in hist]
-        assert lens.tolist() == [len(a) for a, _ in kv]
-        check(out, None, f64(q), kv, new, D ** -0.5, 0, "bf16")
-    assert K.kvq_paged_get_status(c) == 0
+        s.begin(i32(new), n, max(new))
+        for layer in range(layers):
+            qkv = rand((n, cfg.Hq + 2 * cfg.Hkv, D), "bf16", 100 * layer + step)
+            q, k, v = qkv[:, :cfg.Hq], qkv[:, cfg.Hq:cfg.Hq + cfg.Hkv], qkv[:, cfg.Hq + cfg.Hkv:]
+            raw = k.clone()
+            out = torch.empty((n, cfg.Hq, D), dtype=torch.bfloat16, device="cuda")
+            s.attend(layer, q, k, v, D ** -0.5, out)
+            # the rotated keys, within the rotation's tolerance, are what is stored
+            at, h = 0, hist[layer]
+            pos = s.positions.cpu().numpy()
+            angle = pos[:, None].astype(np.float64) * freqs.cpu().numpy()
+            cs, sn = np.cos(angle)[:, None], np.sin(angle)[:, None]
+            u, w = f64(raw)[..., :D // 2], f64(raw)[..., D // 2:]
+            turned = np.concatenate([u * cs - w * sn, w * cs + u * sn], -1)
+            assert np.all(np.abs(f64(k) - turned) <= np.abs(turned) * 2.0 ** -8 + 2.0 ** -18 * (np.abs(u) + np.abs(w)).repeat(2, -1).max())
+            for b, m in enumerate(new):
+                h[b][0].append(R.quantize(f64(k[at:at + m])))
+                h[b][1].append(R.quantize(f64(v[at:at + m])))
+                at += m
+            kv = [(np.concatenate(a), np.concatenate(z)) for a, z in h]
+            assert s.lens.tolist() == [len(a) for a, _ in kv]
+            check(out, None, f64(q), kv, new, D ** -0.5, 0, "bf16")
+        if finish and step in finish:
+            s.finish(i32([b in finish[step] for b in range(B)]))
+            for layer in range(layers):
+                for b in finish[step]:
+                    hist[layer][b] = ([np.zeros((0, cfg.Hkv, D))], [np.zeros((0, cfg.Hkv, D))])
+    assert s.status() == 0
 
 
 @pytest.mark.parametrize("P", [16, 64])
 def test_serving_rounds(P):
-    c = make("bf16", 8, 2, 128, P, 200, 24)
-    serve(c, [[40, 1, 0, 17, 150], [1, 1, 1, 1, 1], [1, 30, 64, 1, 1], [4, 4, 4, 4, 4], [1] * 5])
+    cfg = K.make_paged_cfg(8, 2, 128, P, 60 * 16 // P, 20 * 16 // P, torch.bfloat16)
+    serve(cfg, [[40, 1, 0, 17, 150], [1, 1, 1, 1, 1], [1, 30, 64, 1, 1], [4, 4, 4, 4, 4], [1] * 5, [100, 1, 1, 0, 1], [1] * 5], finish={3: [0, 4], 4: [2]})
 
 
 def test_serving_on_another_stream():
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):
-        serve(make("bf16", 4, 1, 128, 32, 60, 12), [[30, 5, 9, 1, 2], [1, 1, 1, 1, 1]])
+        serve(K.make_paged_cfg(4, 1, 128, 32, 60, 12, torch.bfloat16), [[30, 5, 9, 1, 2], [1, 1, 1, 1, 1]])
     s.synchronize()
 
 
-def test_captured_step_replays():
-    """A decode step as a CUDA graph: plan, append and attention in place, replayed as lengths grow."""
-    B, P, Hq, Hkv, D = 3, 16, 4, 2, 128
-    c = make("bf16", Hq, Hkv, D, P, 40, 8)
-    lens0 = [14, 40, 0]
+@pytest.mark.parametrize("n,lens0,splits", [(1, [14, 40, 0], 0), (1, [14, 40, 0], 3), (3, [2000, 40, 16], 0), (20, [14, 300, 0], 0), (20, [14, 300, 0], 2)])
+def test_captured_step_replays(n, lens0, splits):
+    """A step as a CUDA graph: plan, append and attention in place, replayed as lengths grow."""
+    B, P, Hq, Hkv, D, rounds = 3, 16, 4, 2, 128, 6
+    pages, width = 200, 140
+    c = make("bf16", Hq, Hkv, D, P, pages, width)
     table, kv = fill(c, "bf16", lens0, 3)
     used = sum(-(-a // P) for a in lens0)
-    free = i32(np.concatenate([np.random.RandomState(3).permutation(40)[used:], np.zeros(used)]))
-    n_free, lens, new = i32([40 - used]), i32(lens0), i32([1] * B)
-    q, k, v = (torch.empty((B, h, D), dtype=torch.bfloat16, device="cuda") for h in (Hq, Hkv, Hkv))
-    out, lse = torch.empty_like(q), torch.empty((B, Hq), device="cuda")
-    cu, slots, pos = i32([0] * (B + 1)), i32([0] * B), i32([0] * B)
-    ws = torch.empty(K.kvq_paged_attention_workspace(c.cfg, B, B, 1, 128), dtype=torch.uint8, device="cuda")
-    g = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(g):
+    free = i32(np.concatenate([np.random.RandomState(3).permutation(pages)[used:], np.zeros(used)]))
+    n_free, lens, new = i32([pages - used]), i32(lens0), i32([n] * B)
+    q, k, v = (torch.empty((n * B, h, D), dtype=torch.bfloat16, device="cuda") for h in (Hq, Hkv, Hkv))
+    out, lse = torch.empty_like(q), torch.empty((n * B, Hq), device="cuda")
+    cu, slots, pos = i32([0] * (B + 1)), i32([0] * n * B), i32([0] * n * B)
+    ws = torch.empty(max(16, K.kvq_paged_attention_workspace(c.cfg, B, n * B, n, width * P, splits)), dtype=torch.uint8, device="cuda")
+
+    def step():
         K.kvq_page_plan(c, lens, new, table, free, n_free, cu, lens, n_free, slots, pos)
         K.kvq_paged_append(c, k, v, slots)
-        K.kvq_paged_attention(c, q, None, lens, table, 1, 128, 0.1, out, ws, lse=lse)
+        K.kvq_paged_attention(c, q, cu, lens, table, n, width * P, 0.1, out, ws, lse=lse, splits=splits)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
     hist = [[a, z] for a, z in kv]
-    for step in range(20):
+    for r in range(rounds):
         for x, seed in ((q, 1), (k, 2), (v, 3)):
-            x.copy_(rand(x.shape, "bf16", 50 * step + seed))
-        g.replay()
+            x.copy_(rand(x.shape, "bf16", 50 * r + seed))
+        if r == 2:
+            step()  # the same, launched one by one
+        else:
+            g.replay()
         for b in range(B):
-            hist[b] = [np.concatenate([hist[b][i], R.quantize(f64(x[b:b + 1]))]) for i, x in enumerate((k, v))]
-        assert lens.tolist() == [a + step + 1 for a in lens0]
-        check(out, lse, f64(q), hist, [1] * B, 0.1, 0, "bf16")
+            at = slice(n * b, n * b + n)
+            hist[b] = [np.concatenate([hist[b][i], R.quantize(f64(x[at]))]) for i, x in enumerate((k, v))]
+        assert lens.tolist() == [a + n * (r + 1) for a in lens0]
+        check(out, lse, f64(q), hist, [n] * B, 0.1, 0, "bf16")
     assert K.kvq_paged_get_status(c) == 0
+
+
+def test_two_streams_at_once():
+    """Decode, drafts and chunks of two batches on two streams, each with its own workspace."""
+    runs = []
+    for n, splits, seed in ((1, 3, 1), (4, 0, 2), (70, 2, 3)):
+        c = make("bf16", 8, 2, 128, 32, 300, 100)
+        lens = [3000, 77, 1500]
+        table, kv = fill(c, "bf16", lens, seed)
+        q = rand((3 * n, 8, 128), "bf16", seed + 9)
+        cu, ln = i32([0, n, 2 * n, 3 * n]), i32(lens)
+        ws = torch.empty(K.kvq_paged_attention_workspace(c.cfg, 3, 3 * n, n, 3000, splits), dtype=torch.uint8, device="cuda")
+        alone = torch.empty_like(q)
+        call = lambda out, c=c, q=q, cu=cu, ln=ln, table=table, n=n, ws=ws, splits=splits: K.kvq_paged_attention(  # noqa: E731
+            c, q, cu, ln, table, n, 3000, 0.1, out, ws, splits=splits)
+        call(alone)
+        runs.append((call, alone, torch.empty_like(q), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for call, _, out, s in runs:
+            with torch.cuda.stream(s):
+                call(out)
+    torch.cuda.synchronize()
+    for _, alone, out, _ in runs:
+        assert torch.equal(alone.view(torch.int16), out.view(torch.int16))
