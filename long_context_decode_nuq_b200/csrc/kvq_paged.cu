@@ -89,7 +89,6 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
     extern __shared__ uint32_t s_plan[];  // per request of the chunk: first token, first page, length
     __shared__ long long s_scan[2][32];
     __shared__ int s_used;
-    constexpr int kAtOnce = 4;  // tokens a thread looks up together
     const int tid = threadIdx.x, nt = blockDim.x, chunk = nt * ITEMS;
     uint32_t *s_tok = s_plan, *s_page = s_plan + chunk, *s_len = s_plan + 2 * chunk;  // length: top bit, accepted
     const int rank = blockIdx.x, nc = gridDim.x;  // the grid is one cluster
@@ -147,38 +146,33 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
                 }
         }
         const int ntok = (int)min(tt, max((long long)a.capacity - tok0, 0LL));
-        for (int i = rank * nt + tid; i < ntok; i += kAtOnce * nc * nt) {
-            int slot[kAtOnce], page[kAtOnce];
-            long long pos[kAtOnce];
+        // a warp takes a run of tokens, 32 at a time: one bisection at its start, then the 32 next
+        // boundaries in the lanes' registers, which a token's lane bisects by shuffles
+        const int lane = tid & 31, warps = nc * nt / 32, run = ((ntok + 31) / 32 + warps - 1) / warps * 32;
+        const int i0 = (rank * nt + tid) / 32 * run, i1 = min(ntok, i0 + run);
+        int j0 = i0 < i1 ? find_last(s_tok, m, (uint32_t)i0) : 0;
+        for (int i = i0; i < i1; i += 32) {
+            const uint32_t rel = i + lane, next = j0 + 1 + lane < m ? s_tok[j0 + 1 + lane] : UINT32_MAX;
+            int j = 0;
 #pragma unroll
-            for (int z = 0; z < kAtOnce; ++z) {
-                const int rel = i + z * nc * nt;
-                slot[z] = page[z] = -1;
-                pos[z] = 0;
-                if (rel >= ntok) continue;
-                const int j = find_last(s_tok, m, (uint32_t)rel);
-                const uint32_t lj = s_len[j];
-                const int ln = (int)(lj & 0x7fffffffu);
-                pos[z] = (long long)ln + ((uint32_t)rel - s_tok[j]);
-                if (lj >> 31) {  // accepted, so the position fits
-                    const int pi = (int)(pos[z] >> lp), hv = (int)(((long long)ln + pm) >> lp);
-                    page[z] = pi < hv ? a.table[(size_t)(base + j) * a.max_pages + pi]
-                                      : a.free_pages[n_free - 1 - (int)(page0 + s_page[j] + (pi - hv))];
-                    slot[z] = 0;
-                }
+            for (int step = 16; step; step >>= 1)
+                if (__shfl_sync(0xffffffffu, next, j + step - 1) <= rel) j += step;
+            if (__shfl_sync(0xffffffffu, next, j) <= rel) ++j;
+            j += j0;
+            if (j == j0 + 32) j = find_last(s_tok, m, rel);  // as many requests without tokens
+            j0 = __shfl_sync(0xffffffffu, j, 31);
+            if ((int)rel >= i1) break;
+            const uint32_t lj = s_len[j], ln = lj & 0x7fffffffu, pos = ln + (rel - s_tok[j]);
+            int slot = -1;
+            if (lj >> 31) {  // accepted, so the position fits
+                const int pi = (int)(pos >> lp), hv = (int)((ln + pm) >> lp);
+                const int page = pi < hv ? a.table[(size_t)(base + j) * a.max_pages + pi]
+                                         : a.free_pages[n_free - 1 - ((int)page0 + (int)s_page[j] + (pi - hv))];
+                if (page >= 0 && page < a.num_pages) slot = (page << lp) + (int)(pos & pm);
+                else bad |= KVQ_STATUS_BAD_PAGE;
             }
-#pragma unroll
-            for (int z = 0; z < kAtOnce; ++z) {
-                const int rel = i + z * nc * nt;
-                if (rel >= ntok) break;
-                if (slot[z] == 0) {
-                    const bool in = page[z] >= 0 && page[z] < a.num_pages;
-                    slot[z] = in ? (page[z] << lp) + (int)(pos[z] & pm) : -1;
-                    if (!in) bad |= KVQ_STATUS_BAD_PAGE;
-                }
-                a.slots[tok0 + rel] = slot[z];
-                a.pos[tok0 + rel] = (int32_t)min(pos[z], (long long)INT32_MAX);
-            }
+            a.slots[tok0 + rel] = slot;
+            a.pos[tok0 + rel] = (int32_t)min(pos, (uint32_t)INT32_MAX);
         }
         const long long plast = min(tp, (long long)n_free - page0);
         for (long long r = rank * nt + tid; r < plast; r += (long long)nc * nt) {
