@@ -341,9 +341,9 @@ __global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArg
             const bool mask = got != 3u || t0 + 32 > sg.all_hi || t0 < sg.all_lo;
 
             float sc[2][NT][4];
-            uint32_t kc[2][2][KW], ks[2][2][2];  // codes and scale pairs (s, s) of the lane's channels
 #pragma unroll
             for (int gr = 0; gr < 2; ++gr) {
+                uint32_t kc[2][KW], ks[2][2];
                 const uint8_t* kb = buf + gr * GB;
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
@@ -351,40 +351,33 @@ __global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArg
                     const uint8_t* srow = kb + kGroup * ROW + (tau + 8 * z) * SC;
                     if constexpr (D == 128) {
                         const uint4 x = *reinterpret_cast<const uint4*>(row);
-                        kc[gr][z][0] = x.x, kc[gr][z][1] = x.y, kc[gr][z][2] = x.z, kc[gr][z][3] = x.w;
+                        kc[z][0] = x.x, kc[z][1] = x.y, kc[z][2] = x.z, kc[z][3] = x.w;
                         const uint32_t two = e4m3x2(*reinterpret_cast<const uint16_t*>(srow + 2 * t));
-                        ks[gr][z][0] = __byte_perm(two, 0, 0x1010);
-                        ks[gr][z][1] = __byte_perm(two, 0, 0x3232);
+                        ks[z][0] = __byte_perm(two, 0, 0x1010);
+                        ks[z][1] = __byte_perm(two, 0, 0x3232);
                     } else {
                         const uint2 x = *reinterpret_cast<const uint2*>(row);
-                        kc[gr][z][0] = x.x, kc[gr][z][1] = x.y;
+                        kc[z][0] = x.x, kc[z][1] = x.y;
                         const uint32_t one = srow[t];
-                        ks[gr][z][0] = ks[gr][z][1] = e4m3x2(one | one << 8);
+                        ks[z][0] = ks[z][1] = e4m3x2(one | one << 8);
                     }
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int z = 0; z < 4; ++z) sc[gr][nt][z] = 0.0f;
-            }
 #pragma unroll
-            for (int w = 0; w < KW; ++w) {
-                uint32_t x[2][2][4];
+                for (int w = 0; w < KW; ++w) {
+                    uint32_t x0[4], x1[4];
+                    e2m1x8(kc[0][w], x0);
+                    e2m1x8(kc[1][w], x1);
 #pragma unroll
-                for (int gr = 0; gr < 2; ++gr) {
-                    e2m1x8(kc[gr][0][w], x[gr][0]);
-                    e2m1x8(kc[gr][1][w], x[gr][1]);
-                }
+                    for (int u = 0; u < 2; ++u) {
+                        uint2 qf[NT];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    uint2 qf[NT];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) qf[nt] = s_q[(nt * KS + 2 * w + u) * 32 + lane];
-#pragma unroll
-                    for (int gr = 0; gr < 2; ++gr) {
-                        const uint32_t s0 = ks[gr][0][w * 2 / KW], s1 = ks[gr][1][w * 2 / KW];
-                        const uint32_t A[4] = {hmul2(x[gr][0][2 * u], s0), hmul2(x[gr][1][2 * u], s1),
-                                               hmul2(x[gr][0][2 * u + 1], s0), hmul2(x[gr][1][2 * u + 1], s1)};
+                        for (int nt = 0; nt < NT; ++nt) qf[nt] = s_q[(nt * KS + 2 * w + u) * 32 + lane];
+                        const uint32_t s0 = ks[0][w * 2 / KW], s1 = ks[1][w * 2 / KW];
+                        const uint32_t A[4] = {hmul2(x0[2 * u], s0), hmul2(x1[2 * u], s1), hmul2(x0[2 * u + 1], s0), hmul2(x1[2 * u + 1], s1)};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) mma16816(sc[gr][nt], A, qf[nt].x, qf[nt].y);
                     }
@@ -403,6 +396,21 @@ __global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArg
                             if (!see) sc[gr][nt][z] = -INFINITY;
                         }
             }
+            // V is asked for here, to come while the softmax is computed (4 x 128K 97 -> 94 us)
+            uint32_t vc[2][4][VW], sv[2][4];
+#pragma unroll
+            for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    sv[gr][z] = buf[gr * GB + HALF + kGroup * ROW + g * (D / 8) / kGroup + tv[z] * SC];
+                    const uint8_t* row = buf + gr * GB + HALF + tv[z] * ROW + g * (D / 16);
+                    if constexpr (D == 128) {
+                        const uint2 x = *reinterpret_cast<const uint2*>(row);
+                        vc[gr][z][0] = x.x, vc[gr][z][1] = x.y;
+                    } else {
+                        vc[gr][z][0] = *reinterpret_cast<const uint32_t*>(row);
+                    }
+                }
             // the maximum moves only when some lane's scores ask for it, so the common case needs
             // no exchange between lanes
             float tm[NT][2];
@@ -447,11 +455,7 @@ __global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArg
             }
 #pragma unroll
             for (int gr = 0; gr < 2; ++gr) {
-                const uint8_t* vb = buf + gr * GB + HALF;
-                const uint8_t* vs = vb + kGroup * ROW + g * (D / 8) / kGroup;
-                uint32_t sb[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z) sb[z] = vs[tv[z] * SC];
+                uint32_t sb[4] = {sv[gr][0], sv[gr][1], sv[gr][2], sv[gr][3]};
                 if (mask) {
                     // bytes nobody wrote may hold a NaN scale, and 0 * NaN is not 0
                     const int tg = t0 + gr * kGroup;
@@ -460,25 +464,14 @@ __global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArg
                         if (!(got >> gr & 1u) || tg + tv[z] >= rw.kv) sb[z] = 0;
                 }
                 const uint32_t s01 = e4m3x2(sb[0] | sb[1] << 8), s23 = e4m3x2(sb[2] | sb[3] << 8);
-                uint32_t vc[4][VW];
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const uint8_t* row = vb + tv[z] * ROW + g * (D / 16);
-                    if constexpr (D == 128) {
-                        const uint2 x = *reinterpret_cast<const uint2*>(row);
-                        vc[z][0] = x.x, vc[z][1] = x.y;
-                    } else {
-                        vc[z][0] = *reinterpret_cast<const uint32_t*>(row);
-                    }
-                }
 #pragma unroll
                 for (int w = 0; w < VW; ++w) {
                     // bytes of (token a, token b) codes of one channel: even channels, then odd ones
                     uint32_t e01[4], o01[4], e23[4], o23[4];
-                    e2m1x8((vc[0][w] & 0x0f0f0f0fu) | (vc[1][w] << 4 & 0xf0f0f0f0u), e01);
-                    e2m1x8((vc[0][w] >> 4 & 0x0f0f0f0fu) | (vc[1][w] & 0xf0f0f0f0u), o01);
-                    e2m1x8((vc[2][w] & 0x0f0f0f0fu) | (vc[3][w] << 4 & 0xf0f0f0f0u), e23);
-                    e2m1x8((vc[2][w] >> 4 & 0x0f0f0f0fu) | (vc[3][w] & 0xf0f0f0f0u), o23);
+                    e2m1x8((vc[gr][0][w] & 0x0f0f0f0fu) | (vc[gr][1][w] << 4 & 0xf0f0f0f0u), e01);
+                    e2m1x8((vc[gr][0][w] >> 4 & 0x0f0f0f0fu) | (vc[gr][1][w] & 0xf0f0f0f0u), o01);
+                    e2m1x8((vc[gr][2][w] & 0x0f0f0f0fu) | (vc[gr][3][w] << 4 & 0xf0f0f0f0u), e23);
+                    e2m1x8((vc[gr][2][w] >> 4 & 0x0f0f0f0fu) | (vc[gr][3][w] & 0xf0f0f0f0u), o23);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t A[4] = {hmul2(e01[i], s01), hmul2(o01[i], s01),
