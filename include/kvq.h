@@ -19,7 +19,8 @@
  *     "host".  Cache and workspace buffers must be 16-byte aligned.  The library
  *     allocates no device buffer; its only global state is the fixed scratch array of
  *     kvq_quantize_append_noalloc and the per-thread text of the last CUDA error
- *     (a kvq_step owns host memory and an instantiated CUDA graph).
+ *     (a kvq_step owns host memory and an instantiated CUDA graph), and a note per kernel of the
+ *     devices that have been asked for its shared memory.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
  *     Calls only enqueue work; none synchronizes except kvq_get_status.
  *   - Return value: KVQ_OK (0) or a negative KVQ_ERR_* code.  Argument checks are
@@ -29,7 +30,8 @@
  *     past T_max) set bits in the sticky int32 `status` word of the cache and the
  *     kernel carries on without trapping; read it with kvq_get_status.
  *   - fp16 values travel as their uint16_t bit patterns.
- *   - Only head_dim D = 128 and bits in {2, 3, 4} are supported.
+ *   - Only head_dim D = 128 and bits in {2, 3, 4} are supported; the paged 4-bit cache (below)
+ *     takes D = 64 or 128, the rotation D up to 256.
  */
 #ifndef KVQ_H
 #define KVQ_H
@@ -48,8 +50,8 @@ enum {
     KVQ_ERR_NULL = -1,        /* a required pointer is NULL */
     KVQ_ERR_ALIGN = -2,       /* a device pointer is not 16-byte aligned */
     KVQ_ERR_SHAPE = -3,       /* a dimension or count is out of range */
-    KVQ_ERR_UNSUPPORTED = -4, /* bits or head_dim not supported */
-    KVQ_ERR_RANGE = -5,       /* token range beyond T_max / split count out of range */
+    KVQ_ERR_UNSUPPORTED = -4, /* bits, head_dim, page size or type not supported */
+    KVQ_ERR_RANGE = -5,       /* token range, split count, exponent, scale or axis out of range */
     KVQ_ERR_WORKSPACE = -6,   /* workspace smaller than the size query returned */
     KVQ_ERR_CUDA = -7,        /* a CUDA launch or runtime call failed */
     KVQ_ERR_SCRATCH_LIMIT = -8, /* request exceeds the fixed scratch of kvq_quantize_append_noalloc */
@@ -473,6 +475,10 @@ int kvq_get_status(const kvq_cache* cache, int32_t* out, void* stream);
  * bytes.  A token's slot is page * page_tokens + its row in the page; request b's token t lies in
  * page block_table[b][t / page_tokens].  A value is code * scale * 2^k_exp (v_exp for values); the
  * codes-times-scale product has 6 significant bits, so it is exact in fp16.
+ *
+ * The kernels of this section are launched so that each may start while the one ahead of it in the
+ * stream ends (programmatic dependent launch); each waits for that one before it touches any
+ * buffer, so calls keep their order, in a stream and in a captured graph.
  */
 #define KVQ_F16 0
 #define KVQ_BF16 1

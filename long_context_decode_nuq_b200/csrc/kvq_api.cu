@@ -67,8 +67,9 @@ const char* kvq_strerror(int code) {
         case KVQ_ERR_NULL: return "a required pointer is NULL";
         case KVQ_ERR_ALIGN: return "a device pointer is not 16-byte aligned";
         case KVQ_ERR_SHAPE: return "a dimension or count is out of range";
-        case KVQ_ERR_UNSUPPORTED: return "unsupported bits or head_dim (need D=128, bits 2..4)";
-        case KVQ_ERR_RANGE: return "token range or split count out of range";
+        case KVQ_ERR_UNSUPPORTED:
+            return "unsupported bits, head_dim, page size or type (NUQ cache: D=128, bits 2..4)";
+        case KVQ_ERR_RANGE: return "token range, split count, exponent, scale or axis out of range";
         case KVQ_ERR_WORKSPACE: return "workspace too small";
         case KVQ_ERR_CUDA: return g_cuda_msg;
         case KVQ_ERR_SCRATCH_LIMIT:
