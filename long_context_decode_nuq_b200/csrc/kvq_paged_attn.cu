@@ -86,9 +86,9 @@ __device__ __forceinline__ Seg seg_of(const AttnArgs& a, int b) {
     s.rw = rows_of(a, b);
     s.first = s.rw.len - s.rw.n;
     s.hi = min(s.rw.kv, s.first + s.rw.nq);
-    s.lo = a.window > 0 ? max(0, s.first + 1 - a.window) : 0;
+    s.lo = first_seen(a, s.first);
     s.all_hi = min(s.rw.kv, s.first + 1);
-    s.all_lo = a.window > 0 ? max(0, s.first + s.rw.nq - a.window) : 0;
+    s.all_lo = first_seen(a, s.first + s.rw.nq - 1);
     s.tbase = s.lo & ~(kGroup - 1);
     // one that sees nothing still has a unit, which writes its zeros
     s.u = s.rw.R == 0 ? 0 : s.hi > s.lo ? (s.hi - s.tbase + kUnit - 1) / kUnit : 1;
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArg
                         for (int z = 0; z < 4; ++z) {
                             const int tok = t0 + gr * kGroup + tau + (z & 2) * 4;
                             const int p = pos[nt][z & 1];
-                            const bool see = (got >> gr & 1u) && tok < ts1 && tok <= p && (a.window <= 0 || tok > p - a.window);
+                            const bool see = (got >> gr & 1u) && tok < ts1 && tok <= p && tok >= first_seen(a, p);
                             if (!see) sc[gr][nt][z] = -INFINITY;
                         }
             }

@@ -40,6 +40,11 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs& a, int b) {
     return r;
 }
 
+// The first token that a query at position p sees (p - window may pass 32 bits, p being negative).
+__device__ __forceinline__ int first_seen(const AttnArgs& a, int p) {
+    return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
+}
+
 template <bool BF>
 __device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack16<BF>(a, b), pack16<BF>(c, d));

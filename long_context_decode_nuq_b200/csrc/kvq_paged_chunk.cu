@@ -176,9 +176,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
     const int i0 = r0 / G, i1 = (r0 + rows - 1) / G;
     const int first = rw.len - rw.n;
     const int hi = min(rw.kv, first + i1 + 1);
-    const int lo = a.window > 0 ? max(0, first + i0 + 1 - a.window) : 0;
+    const int lo = first_seen(a, first + i0);
     const int all_hi = min(rw.kv, first + i0 + 1);
-    const int all_lo = a.window > 0 ? max(0, first + i1 + 1 - a.window) : 0;
+    const int all_lo = first_seen(a, first + i1);
     const int tbase = lo & ~(kGroup - 1);
     const int tiles = hi > lo ? (hi - tbase + kTok - 1) / kTok : 0;
     const int tb = (int)((int64_t)tiles * s / a.S);
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, in bits 16 and up
         const uint32_t st = tmem + lanes + i * 128, ot = tmem + lanes + 256 + i * D;
         const int pos = first + r / G;
-        const int hi_r = min(rw.kv, pos + 1), lo_r = a.window > 0 ? pos + 1 - a.window : 0;
+        const int hi_r = min(rw.kv, pos + 1), lo_r = first_seen(a, pos);
         if (i < nact)
             for (int j = 0; j < n; ++j) {
                 if (!__all_sync(0xffffffffu, wait_on(&s_full[i], j & 1, dead))) break;

@@ -263,6 +263,10 @@ CASES = [
     ("bf16", 64, 64, 1, 3, [500, 77, 300], [9, 9, 130], 33, 0),
     ("bf16", 128, 64, 1, 4, [500, 77, 300], [200, 77, 130], 100, 3),
     ("fp16", 128, 16, 1, 1, [2000], [300], 10000, 0),
+    # the widest window, with queries before the first token
+    ("bf16", 128, 16, 1, 2, [3, 0, 20], [8, 5, 8], 2 ** 31 - 1, 0),
+    ("fp16", 64, 16, 1, 1, [3, 700, 2], [9, 1, 2], 2 ** 31 - 1, 2),
+    ("bf16", 128, 16, 1, 4, [3, 0, 60], [140, 33, 129], 2 ** 31 - 1, 0),
     # long ones, by the library's choice: a line of units cut anywhere, several splits
     ("bf16", 128, 64, 2, 4, [6000, 1, 900], [1, 1, 1], 0, 0),
     ("fp16", 64, 32, 1, 2, [9000, 40, 0, 2500], [8, 8, 8, 5], 0, 0),
