@@ -493,7 +493,8 @@ typedef struct kvq_paged_cfg {
     int32_t D;           /* head dimension, 64 or 128 */
     int32_t page_tokens; /* 16, 32, 64 or 128 */
     int32_t num_pages;   /* pages of the pool; num_pages * page_tokens < 2^31 */
-    int32_t max_pages;   /* row width of the block tables: pages a request may have */
+    int32_t max_pages;   /* row width of the block tables: pages a request may have;
+                            max_pages * page_tokens < 2^31 - 4096 */
     int32_t dtype;       /* KVQ_F16 or KVQ_BF16: keys, values, queries and outputs */
     int32_t k_exp;       /* keys are stored divided by 2^k_exp, -64 .. 64: E4M3 scales reach from */
     int32_t v_exp;       /* 2^-9 to 448, so a 16-channel maximum of 0.012 .. 2688 fits with 0 */
@@ -525,8 +526,8 @@ int kvq_paged_get_status(const kvq_paged_cache* cache, int32_t* out, void* strea
  * tokens get slot -1, and KVQ_STATUS_NO_PAGES (too few pages) or KVQ_STATUS_LEN_OVERFLOW is set.
  * Once the list has run out no later request gets a page; one that needs none is still accepted.
  *   len, n_new   int32 [B] (negative counts as 0);  block_table int32 [B][max_pages], updated
- *   free_pages   int32 [num_pages], read;  n_free int32 [1], entries in use
- *   capacity     host: entries of slots and positions
+ *   free_pages   int32, its first n_free entries are read;  n_free int32 [1], entries in use
+ *   capacity     host: entries of slots and positions, at most 2^30
  * Outputs (device):
  *   cu_new int32 [B+1]  exclusive prefix sum of n_new: request b's tokens are
  *                       [cu_new[b], cu_new[b+1]) of the step's packed token list
@@ -545,7 +546,9 @@ int kvq_page_plan(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_
  * Give back the pages of finished requests: for each b with done[b] != 0, in request order, its
  * ceil(len[b]/P) pages go on top of the free list in table order, their table entries become -1
  * and len[b] becomes 0.  n_free is updated in place.  Pages that would pass num_pages entries are
- * dropped and set KVQ_STATUS_BAD_PAGE.
+ * dropped and set KVQ_STATUS_BAD_PAGE.  A page that stands in two tables would be given back
+ * twice: while requests share one, who may release it is the caller's to count.
+ *   free_pages   int32 [num_pages]
  */
 int kvq_page_release(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_t B,
                      int32_t* len, const int32_t* done, int32_t* block_table, int32_t* free_pages,
@@ -579,7 +582,7 @@ int kvq_paged_dequantize(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache,
  * n_b = cu_q[b+1] - cu_q[b] of its len[b] cached tokens: query i stands at position
  * p = len[b] - n_b + i and sees the tokens t <= p, with window > 0 only those t > p - window.
  *   x_t = sm_scale * q . khat_t,  out = sum_t e^(x_t - lse) vhat_t,  lse = log sum_t e^(x_t)
- * over the seen tokens; a query that sees none (p < 0) gets out = 0, lse = -inf.  Pages numbered
+ * over the seen tokens (sm_scale * 2^k_exp within binary32); a query that sees none (p < 0) gets out = 0, lse = -inf.  Pages numbered
  * outside the pool count as not seen and set KVQ_STATUS_BAD_PAGE.
  *   q     16-bit [total_q][Hq][D], rows q_stride elements apart (a multiple of 8, at least Hq*D),
  *         16-byte aligned;  out 16-bit [total_q][Hq][D];  lse float [total_q][Hq] or NULL
@@ -616,7 +619,7 @@ int kvq_paged_attention_workspace(const kvq_paged_cfg* cfg, int32_t B, int32_t t
  *   positions int32 [axes][n];  freqs double [rot_dim/2] (device)
  */
 typedef struct kvq_rope_cfg {
-    int32_t Hq, Hkv;    /* Hq >= 1, Hkv >= 0 */
+    int32_t Hq, Hkv;    /* 1 .. 65536, 0 .. 65536 */
     int32_t D;          /* a multiple of 16, 16 .. 256 */
     int32_t rot_dim;    /* a multiple of 16, 16 .. D */
     int32_t dtype;      /* KVQ_F16, KVQ_BF16 or KVQ_F32 */

@@ -17,7 +17,8 @@ int check_paged_cfg(const kvq_paged_cfg* c) {
     if (c->Hq < c->Hkv || c->Hq % c->Hkv != 0 || c->Hq / c->Hkv > 64) return KVQ_ERR_SHAPE;
     if (c->num_pages < 1 || c->max_pages < 1) return KVQ_ERR_SHAPE;
     if ((int64_t)c->num_pages * c->page_tokens > INT32_MAX) return KVQ_ERR_SHAPE;
-    if ((int64_t)c->max_pages * c->page_tokens > INT32_MAX) return KVQ_ERR_SHAPE;
+    // a tile may begin before a request's last token and end a few hundred past it, in 32 bits
+    if ((int64_t)c->max_pages * c->page_tokens > INT32_MAX - 4096) return KVQ_ERR_SHAPE;
     if (c->k_exp < -64 || c->k_exp > 64 || c->v_exp < -64 || c->v_exp > 64) return KVQ_ERR_RANGE;
     return KVQ_OK;
 }
@@ -488,7 +489,7 @@ int kvq_page_plan(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_
         !cu_new || !len_out || !n_free_out)
         return KVQ_ERR_NULL;
     if (capacity > 0 && (!slots || !positions)) return KVQ_ERR_NULL;
-    if (B < 1 || B > (1 << 20) || capacity < 0) return KVQ_ERR_SHAPE;
+    if (B < 1 || B > (1 << 20) || capacity < 0 || capacity > (1 << 30)) return KVQ_ERR_SHAPE;
     PlanArgs a{len,    n_new, free_pages, n_free, block_table,      cu_new,         len_out,        n_free_out, slots,
                positions, cache->status, B, cfg->page_tokens, cfg->num_pages, cfg->max_pages, capacity};
     // a thread a request or token; one block up to 4096 tokens, since a cluster's start and its

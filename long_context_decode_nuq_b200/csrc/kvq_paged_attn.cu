@@ -816,7 +816,8 @@ int kvq_paged_attention(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, 
     if (e) return e;
     if ((e = check_paged_cache(cache))) return e;
     if ((e = check_sizes(cfg, B, total_q, max_q, max_len, splits))) return e;
-    if (window < 0 || !isfinite(sm_scale)) return KVQ_ERR_RANGE;
+    const float scale_log2 = (float)ldexp((double)sm_scale * 1.4426950408889634, cfg->k_exp);
+    if (window < 0 || !isfinite(scale_log2)) return KVQ_ERR_RANGE;
     if (!cu_q && (total_q != B || max_q != 1)) return KVQ_ERR_SHAPE;
     if (total_q == 0) return KVQ_OK;
     if (!q || !len || !block_table || !out) return KVQ_ERR_NULL;
@@ -849,7 +850,7 @@ int kvq_paged_attention(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, 
         }
     }
     a.total_q = total_q, a.max_q = max_q, a.max_len = max_len, a.window = window, a.S = p.S;
-    a.scale_log2 = (float)ldexp((double)sm_scale * 1.4426950408889634, cfg->k_exp);
+    a.scale_log2 = scale_log2;
     a.out_scale = ldexpf(1.0f, cfg->v_exp);
     const bool bf = cfg->dtype == KVQ_BF16;
     cudaStream_t st = (cudaStream_t)stream;

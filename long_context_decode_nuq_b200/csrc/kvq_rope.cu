@@ -162,7 +162,7 @@ extern "C" int kvq_rope(const kvq_rope_cfg* cfg, const void* q, int64_t q_stride
     // few tokens: the heads over several blocks, one head a thread
     int gy = 1;
     if (n < 148 * 2) gy = (heads + lanes - 1) / lanes;
-    const dim3 grid((n + a.tokens - 1) / a.tokens, gy);
+    const dim3 grid((unsigned)(((int64_t)n + a.tokens - 1) / a.tokens), gy);
     const size_t smem = (size_t)a.tokens * (cfg->rot_dim / 2) * sizeof(float2);
     cudaStream_t st = (cudaStream_t)stream;
     const bool adj = cfg->adjacent;

@@ -19,7 +19,8 @@ def cfg(**kw):
 @pytest.mark.parametrize("kw,code", [
     ({}, 0), (dict(D=96), UNSUPPORTED), (dict(page_tokens=48), UNSUPPORTED), (dict(page_tokens=256), UNSUPPORTED), (dict(dtype=2), UNSUPPORTED),
     (dict(Hkv=0), SHAPE), (dict(Hkv=3), SHAPE), (dict(Hq=1), SHAPE), (dict(Hq=130), SHAPE), (dict(num_pages=0), SHAPE), (dict(max_pages=0), SHAPE),
-    (dict(num_pages=1 << 27), SHAPE), (dict(max_pages=1 << 27), SHAPE), (dict(k_exp=65), RANGE), (dict(v_exp=-65), RANGE)])
+    (dict(num_pages=1 << 27), SHAPE), (dict(max_pages=1 << 27), SHAPE), (dict(max_pages=(1 << 27) - 256), SHAPE), (dict(max_pages=(1 << 27) - 257), 0),
+    (dict(k_exp=65), RANGE), (dict(v_exp=-65), RANGE)])
 def test_config(kw, code):
     c = cfg(**kw)
     assert K.kvq_paged_validate_cfg(c) == code
@@ -56,7 +57,7 @@ def test_dequantize(change, code):
 
 
 @pytest.mark.parametrize("change,code", [
-    ({1: None}, NULL), ({2: 0}, SHAPE), ({2: (1 << 20) + 1}, SHAPE), ({3: None}, NULL), ({5: None}, NULL), ({8: -1}, SHAPE), ({9: None}, NULL),
+    ({1: None}, NULL), ({2: 0}, SHAPE), ({2: (1 << 20) + 1}, SHAPE), ({3: None}, NULL), ({5: None}, NULL), ({8: -1}, SHAPE), ({8: (1 << 30) + 1}, SHAPE), ({9: None}, NULL),
     ({12: None}, NULL), ({13: None}, NULL)])
 def test_plan(change, code):
     a = [ctypes.byref(cfg()), cache(), 3, A, A, A, A, A, 7, A, A, A, A, A, None]
@@ -76,7 +77,7 @@ def test_release(change, code):
 @pytest.mark.parametrize("change,code", [
     ({1: None}, NULL), ({2: None}, NULL), ({2: A + 8}, ALIGN), ({3: 1020}, ALIGN), ({3: 1016}, SHAPE), ({4: None}, SHAPE), ({5: 0}, SHAPE),
     ({5: 70000}, SHAPE), ({6: -1}, SHAPE), ({6: 0}, 0), ({7: None}, NULL), ({8: None}, NULL), ({9: 0}, SHAPE), ({10: 0}, SHAPE),
-    ({11: float("nan")}, RANGE), ({11: float("inf")}, RANGE), ({12: -1}, RANGE), ({13: A + 2}, ALIGN), ({13: None}, NULL), ({15: None}, NULL),
+    ({11: float("nan")}, RANGE), ({11: float("inf")}, RANGE), ({11: 3e38}, RANGE), ({12: -1}, RANGE), ({13: A + 2}, ALIGN), ({13: None}, NULL), ({15: None}, NULL),
     ({15: A + 8}, ALIGN), ({16: 10}, WORKSPACE), ({17: 257}, RANGE), ({17: -1}, RANGE)])
 def test_attention(change, code):
     a = [ctypes.byref(cfg()), cache(), A, 1024, A, 3, 9, A, A, 4, 640, 0.1, 0, A, None, A, 1 << 30, 2, None]
