@@ -714,6 +714,11 @@ int chunk_splits(const kvq_paged_cfg* c, int64_t units, int64_t tiles) {
     return best;
 }
 
+// Most tokens of a split of the chunk kernel.  The tensor cores cut their binary32 sums off instead
+// of rounding them, so O drifts toward 0 with every 16 tokens added: by 8e-4 of itself over 2^20
+// tokens of like sign (measured), by 1e-4, a fifth of fp16's half step, over 2^17.
+constexpr int kSplitTokens = 1 << 17;
+
 Plan plan_of(const kvq_paged_cfg* c, int B, int max_q, int max_len, int splits, int window) {
     const int64_t R = (int64_t)max_q * (c->Hq / c->Hkv);
     // no row block sees more tokens than this
@@ -730,6 +735,8 @@ Plan plan_of(const kvq_paged_cfg* c, int B, int max_q, int max_len, int splits, 
             const int S = chunk_splits(c, units, ((int64_t)max_len + 127) / 128);
             if (S < p.S) p.S = S;
         }
+        const int64_t least = (span + kSplitTokens - 1) / kSplitTokens;
+        if (p.S < least) p.S = (int)least;
         p.join = p.S > 1;
         return p;
     }

@@ -308,6 +308,28 @@ def test_attention(dtype, D, P, Hkv, G, lens, news, window, splits):
         assert torch.equal(out.view(torch.int16), again.view(torch.int16))
 
 
+@pytest.mark.parametrize("n,splits", [(1, 0), (20, 0), (20, 1)])
+def test_attention_over_millions_of_tokens(n, splits):
+    """Equal weights over values of one sign, whose sums only grow.  Tolerance: the output's half
+    step, and for 2^17 / 16 sums in a row at most a step of binary32 (2^-23) each."""
+    T, P, D = 1 << 22, 128, 64
+    c = make("fp16", 1, 1, D, P, T // P, T // P)
+    v = torch.rand((T, 1, D), generator=torch.Generator("cuda").manual_seed(1), device="cuda", dtype=torch.float16) + 0.5
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    K.kvq_paged_append(c, torch.zeros_like(v), v, slots)
+    kh = torch.empty_like(v)
+    K.kvq_paged_dequantize(c, slots, kh, v)
+    q, out, lse = rand((n, 1, D), "fp16", 2), torch.empty((n, 1, D), dtype=torch.float16, device="cuda"), torch.empty((n, 1), device="cuda")
+    ws = torch.empty(max(16, K.kvq_paged_attention_workspace(c.cfg, 1, n, n, T, splits)), dtype=torch.uint8, device="cuda")
+    K.kvq_paged_attention(c, q, i32([0, n]), i32([T]), slots[:T // P].view(1, -1), n, T, 1.0, out, ws, lse=lse, splits=splits)
+    for i in (0, n - 1):
+        seen = T - n + 1 + i
+        want = v[:seen, 0].mean(0, dtype=torch.float64)
+        assert ((out[i, 0].double() - want).abs() <= want * (2.0 ** -11 * 1.01 + 2.0 ** 13 * 2.0 ** -23)).all()
+        assert abs(lse[i, 0].item() - np.log(seen)) <= 2.0 ** -22 * (np.log(seen) + 20)
+    assert K.kvq_paged_get_status(c) == 0
+
+
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("size", [1e-30, 1e-3, 1e3])
 @pytest.mark.parametrize("n", [1, 40])

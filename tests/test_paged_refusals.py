@@ -94,6 +94,10 @@ def test_workspace_sizes():
     n = [K.kvq_paged_attention_workspace(cfg(), 3, 600, 200, 5000, s) for s in (1, 2, 256)]
     assert n == [0, 2 * 600 * 8 * 130 * 4, 256 * 600 * 8 * 130 * 4]
     assert K.kvq_paged_attention_workspace(cfg(), 3, 3, 1, 64) == 0
+    # and no split of more than 2^17 tokens
+    wide = cfg(max_pages=1 << 16)
+    n = [K.kvq_paged_attention_workspace(wide, 3, 600, 200, t, 1) for t in (1 << 17, (1 << 17) + 1, 1 << 20)]
+    assert n == [0, 2 * 600 * 8 * 130 * 4, 8 * 600 * 8 * 130 * 4]
 
 
 @pytest.mark.parametrize("kw,change,code", [
