@@ -650,17 +650,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_paged_join(const AttnArgs a
     if (threadIdx.x == 0 && a.lse) a.lse[grow] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-// Joins the chunk kernel's splits of a row, in split order: a warp per row.
+// Joins the chunk kernel's splits of a row, in split order: a warp per row of the units that were
+// split.
 constexpr int kMergeWarps = 4;
 template <int D, bool BF>
 __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const AttnArgs a) {
-    const int h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31;
+    constexpr int PB = kChunkRows / kMergeWarps;  // blocks of a unit
+    const Unit unit = unit_of(a, a.whole + (int)blockIdx.x / PB);
+    const int h = unit.h, b = unit.b, lane = threadIdx.x & 31;
     const int G = a.c.Hq / a.c.Hkv;
     let_next();
     after_previous();
     const Rows rw = rows_of(a, b);
     const int64_t nrow = (int64_t)a.total_q * a.c.Hq;
-    const int r = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    const int r = unit.rb * kChunkRows + (int)blockIdx.x % PB * kMergeWarps + (threadIdx.x >> 5);
     if (r >= rw.R) return;
     const int64_t grow = (int64_t)(rw.c0 + r / G) * a.c.Hq + h * G + r % G;
     float M = -INFINITY;
@@ -690,7 +693,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const AttnArgs
 struct Plan {
     int nt;   // 8-row tiles of k_paged_attn; 0: the chunk kernel
     int nrb;  // chunk kernel: row blocks
-    int S;    // chunk kernel: splits;  k_paged_attn: blocks, or blocks of a cluster
+    int64_t units, whole;  // chunk kernel: row blocks of all (request, kv head)s; those not split
+    int S;    // chunk kernel: splits of the other units;  k_paged_attn: blocks, or blocks of a cluster
     bool cluster;
     bool join;
 };
@@ -699,19 +703,22 @@ constexpr int kSms = 148;
 // More rows of a kv head than this go to the chunk kernel.
 constexpr int kFewRows = 16;
 
-// Splits of the chunk kernel: the least time of a model in which a block costs 10 us and 2 us per
-// 128 tokens (measured: 2.0), blocks run one per SM in waves, and a split writes and reads its part
-// at 5 TB/s.  256 queries against 32768 tokens, 8 kv heads: 514 us in one part, 68 us in 18.
-int chunk_splits(const kvq_paged_cfg* c, int64_t units, int64_t tiles) {
-    int best = 1;
-    double least = 1e30;
-    for (int S = 1; S <= kSms && S <= tiles; ++S) {
-        const int64_t waves = (units * S + kSms - 1) / kSms;
-        double t = (double)waves * (10.0 + 2.0 * (double)((tiles + S - 1) / S));
-        if (S > 1) t += 4.0 + (double)units * S * kChunkRows * c->D * 8 / 5e6;
-        if (t < 0.98 * least) least = t, best = S;
-    }
-    return best;
+// How the chunk kernel's units (256 rows of a kv head each) are spread: the first `whole` get a
+// block each, the others S, whose parts k_paged_merge adds.  The least time of a model in which a
+// block costs 10 us and 2 us per 128 tokens (measured: 2.0), blocks run one per SM in waves, and a
+// split writes and reads its part at 5 TB/s; whole units come in full waves.
+void chunk_splits(const kvq_paged_cfg* c, int64_t units, int64_t tiles, int64_t* whole, int* splits) {
+    *whole = units, *splits = 1;
+    const int64_t waves = units / kSms;
+    double least = (double)((units + kSms - 1) / kSms) * (10.0 + 2.0 * (double)tiles);
+    for (int64_t w = waves; w >= 0; w = w == 0 ? -1 : w == waves ? w - 1 : 0)  // all full waves whole, one less, none
+        for (int S = 2; S <= kSms && S <= tiles; ++S) {
+            const int64_t rest = units - w * kSms;
+            if (rest == 0) break;
+            const double t = (double)w * (10.0 + 2.0 * (double)tiles) + 4.0 + (double)rest * S * kChunkRows * c->D * 8 / 5e6 +
+                             (double)((rest * S + kSms - 1) / kSms) * (10.0 + 2.0 * (double)((tiles + S - 1) / S));
+            if (t < 0.98 * least) least = t, *whole = w * kSms, *splits = S;
+        }
 }
 
 // Most tokens of a split of the chunk kernel.  The tensor cores cut their binary32 sums off instead
@@ -727,16 +734,22 @@ Plan plan_of(const kvq_paged_cfg* c, int B, int max_q, int max_len, int splits, 
     Plan p{};
     p.nt = R <= 8 ? 1 : R <= kFewRows ? 2 : 0;
     p.nrb = p.nt ? 1 : (int)((R + kChunkRows - 1) / kChunkRows);
-    const int64_t units = (int64_t)B * c->Hkv * p.nrb;
+    const int64_t units = p.units = (int64_t)B * c->Hkv * p.nrb;
     if (p.nt == 0) {
-        p.S = splits ? splits : chunk_splits(c, units, (span + 127) / 128);
-        // the workspace is sized without the window, which must not raise the splits
-        if (!splits && span < max_len) {
-            const int S = chunk_splits(c, units, ((int64_t)max_len + 127) / 128);
+        p.whole = 0, p.S = splits;
+        if (!splits) {
+            chunk_splits(c, units, (span + 127) / 128, &p.whole, &p.S);
+            // the workspace is sized without the window, which must not raise the splits
+            int64_t whole;
+            int S = p.S;
+            if (span < max_len) chunk_splits(c, units, ((int64_t)max_len + 127) / 128, &whole, &S);
             if (S < p.S) p.S = S;
         }
-        const int64_t least = (span + kSplitTokens - 1) / kSplitTokens;
-        if (p.S < least) p.S = (int)least;
+        if (span > kSplitTokens) {
+            const int64_t least = (span + kSplitTokens - 1) / kSplitTokens;
+            p.whole = 0, p.S = (int)(p.S < least ? least : p.S);
+        }
+        if (p.S == 1) p.whole = units;
         p.join = p.S > 1;
         return p;
     }
@@ -831,7 +844,9 @@ int kvq_paged_attention(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, 
     if (!aligned16(q) || !aligned16(out) || (q_stride & 7)) return KVQ_ERR_ALIGN;
     if (q_stride < (int64_t)cfg->Hq * cfg->D) return KVQ_ERR_SHAPE;
     const Plan p = plan_of(cfg, B, max_q, max_len, splits, window);
-    if ((int64_t)p.S * p.nrb > INT32_MAX) return KVQ_ERR_RANGE;
+    // blocks of the chunk kernel and of its merge
+    const int64_t per_unit = !p.join ? 1 : p.S > kChunkRows / kMergeWarps ? p.S : kChunkRows / kMergeWarps;
+    if (p.nt == 0 && p.units * per_unit > INT32_MAX) return KVQ_ERR_RANGE;
     const size_t need = ws_bytes(cfg, p, B, total_q);
     if (need > 0) {
         if (!workspace) return KVQ_ERR_NULL;
@@ -862,12 +877,12 @@ int kvq_paged_attention(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, 
     const bool bf = cfg->dtype == KVQ_BF16;
     cudaStream_t st = (cudaStream_t)stream;
     if (p.nt == 0) {
-        if ((e = run_chunk(a, p.nrb, B, st))) return e;
+        a.whole = (int)p.whole, a.B = B, a.nrb = p.nrb;
+        if ((e = run_chunk(a, st))) return e;
         if (p.join) {
             auto* mk = cfg->D == 64 ? (bf ? k_paged_merge<64, true> : k_paged_merge<64, false>)
                                     : (bf ? k_paged_merge<128, true> : k_paged_merge<128, false>);
-            const int64_t R = (int64_t)max_q * (cfg->Hq / cfg->Hkv);
-            return launch_overlapped(mk, dim3((unsigned)((R + kMergeWarps - 1) / kMergeWarps), cfg->Hkv, B), kMergeWarps * 32, 0, 1, st, a);
+            return launch_overlapped(mk, dim3((unsigned)((p.units - p.whole) * (kChunkRows / kMergeWarps))), kMergeWarps * 32, 0, 1, st, a);
         }
         return KVQ_OK;
     }

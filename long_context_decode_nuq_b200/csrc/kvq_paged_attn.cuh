@@ -21,7 +21,10 @@ struct AttnArgs {
     float2* pml;
     int4* rec;        // few-row kernel: what k_paged_join has to join, or NULL
     bool by_request;  // a record per (request, kv head), else per block
-    int32_t total_q, max_q, max_len, window, S;
+    int32_t total_q, max_q, max_len, window;
+    int32_t S;         // splits (chunk kernel, of the units behind the whole ones); blocks of a cluster
+    int32_t whole;     // chunk kernel: units that one block does alone
+    int32_t B, nrb;    // chunk kernel: requests, row blocks of a (request, kv head)
     float scale_log2, out_scale;
 };
 
@@ -45,6 +48,15 @@ __device__ __forceinline__ int first_seen(const AttnArgs& a, int p) {
     return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
 }
 
+// Chunk kernel and merge: unit u is row block rb of (b, h), the row blocks that see most first.
+struct Unit {
+    int rb, b, h;
+};
+__device__ __forceinline__ Unit unit_of(const AttnArgs& a, int u) {
+    const int seg = u % (a.B * a.c.Hkv);
+    return {a.nrb - 1 - u / (a.B * a.c.Hkv), seg / a.c.Hkv, seg % a.c.Hkv};
+}
+
 template <bool BF>
 __device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack16<BF>(a, b), pack16<BF>(c, d));
@@ -55,5 +67,5 @@ __device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, f
 namespace kvq_host {
 // Prompt chunks (kvq_paged_chunk.cu): query rows of a block, and the launch.
 constexpr int kChunkRows = 256;
-int run_chunk(const kvq::AttnArgs& a, int nrb, int B, cudaStream_t stream);
+int run_chunk(const kvq::AttnArgs& a, cudaStream_t stream);
 }  // namespace kvq_host

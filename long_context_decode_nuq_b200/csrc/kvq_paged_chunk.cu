@@ -7,8 +7,9 @@ using namespace kvq_host;
 namespace {
 
 // ---------------------------------------------------------------------------------
-// A block takes 256 query rows of one (request, kv head), as two tiles of 128, and one split of
-// the tokens they see, 128 tokens at a time.  Tensor memory holds, per tile, the scores S [128 x
+// A block takes 256 query rows of one (request, kv head), as two tiles of 128, and all of the
+// tokens they see or, for the units that would not fill a last wave, one split of them, 128 tokens
+// at a time.  Tensor memory holds, per tile, the scores S [128 x
 // 128] and O [128 x D] in binary32; P overwrites S as fp16 and is the second product's operand
 // from there.  Roles, by warp:
 //   0-3, 4-7   softmax of a row tile, a thread a row: scores out of tensor memory, maximum, e^x,
@@ -40,7 +41,7 @@ struct Smem {
     static constexpr int raw = slot + kSlots * slot_bytes;   // [kRaw][8 groups]: keys or values
     static constexpr int raw_bytes = kTok / kGroup * Paged<D>::kHalf;
     static constexpr int bar = raw + kRaw * raw_bytes;
-    static constexpr int n_bar = 2 * kRaw + 2 * kSlots + 8;
+    static constexpr int n_bar = 2 * kRaw + 2 * kSlots + 9;
     static constexpr int misc = bar + 8 * n_bar;             // tmem address, dead flag, group masks
     static constexpr int total = misc + 64;
 };
@@ -147,7 +148,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) 
         : "memory");
 }
 template <int D, bool BF>
-__global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, int nrb) {
+__global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a) {
     using L = Smem<D>;
     constexpr int GPT = kTok / kGroup;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -158,18 +159,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
     uint64_t* s_full = kv_empty + kSlots;  // [2]
     uint64_t* p_full = s_full + 2;         // [2][2]: P's first and second 64 columns
     uint64_t* pv_done = p_full + 4;        // [2]
+    uint64_t* q_full = pv_done + 2;
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + L::misc);
     volatile int* dead = reinterpret_cast<volatile int*>(smem + L::misc + 4);
     uint8_t* gmask = smem + L::misc + 8;   // [8] groups that were brought, of the last 8 tiles
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int s = blockIdx.x % a.S, rb = nrb - 1 - blockIdx.x / a.S, h = blockIdx.y, b = blockIdx.z;
+    const int cut = (int)blockIdx.x - a.whole, S = cut < 0 ? 1 : a.S, s = cut < 0 ? 0 : cut % S;
+    const Unit unit = unit_of(a, cut < 0 ? (int)blockIdx.x : a.whole + cut / S);
+    const int rb = unit.rb, h = unit.h, b = unit.b;
     const int G = a.c.Hq / a.c.Hkv, P = a.c.page_tokens;
     let_next();
     after_previous();
     const Rows rw = rows_of(a, b);
     const int r0 = rb * kRows;
-    if (threadIdx.x == 0 && h == 0 && blockIdx.x == 0 && (rw.n > rw.nq || rw.len > rw.kv))
+    if (threadIdx.x == 0 && h == 0 && rb == 0 && s == 0 && (rw.n > rw.nq || rw.len > rw.kv))
         set_status(a.status, KVQ_STATUS_LEN_OVERFLOW);
     if (r0 >= rw.R) return;
     const int rows = min(kRows, rw.R - r0), nact = rows > 128 ? 2 : 1;
@@ -181,8 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
     const int all_lo = first_seen(a, first + i1);
     const int tbase = lo & ~(kGroup - 1);
     const int tiles = hi > lo ? (hi - tbase + kTok - 1) / kTok : 0;
-    const int tb = (int)((int64_t)tiles * s / a.S);
-    const int n = (int)((int64_t)tiles * (s + 1) / a.S) - tb;  // steps of this block
+    const int tb = (int)((int64_t)tiles * s / S);
+    const int n = (int)((int64_t)tiles * (s + 1) / S) - tb;  // steps of this block
     const int tok0 = tbase + tb * kTok;
 
     if (warp == 13) {
@@ -195,47 +199,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
         for (int i = 0; i < kSlots; ++i) mbar_init(&kv_full[i], 4), mbar_init(&kv_empty[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&pv_done[i], 1);
         for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 4);
+        mbar_init(q_full, 8);
         fence_mbar_init();
-    }
-    // queries: a thread a row, its power of two kept for the scores
-    const int row = threadIdx.x;  // of the block, for warps 0-7
-    const int r = r0 + row;
-    float sl2 = 0.0f;
-    if (warp < 8) {
-        const bool real = r < rw.R;
-        const uint16_t* src = a.q + (int64_t)(rw.c0 + (real ? r / G : 0)) * a.qs + (h * G + (real ? r % G : 0)) * D;
-        int e = 0;
-        if (BF && real) {
-            uint32_t mx = 0;
-            for (int i = 0; i < D / 8; ++i) {
-                const uint4 x = reinterpret_cast<const uint4*>(src)[i];
-                mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-            }
-            const int eb = (int)(max(mx & 0xffffu, mx >> 16) >> 7);
-            if (eb < 255) e = max(eb - 127 - 10, -120);
-        }
-        // a negative scale goes into the query, so that the largest score is the largest product
-        const float f = __uint_as_float((uint32_t)(127 - e) << 23) * (a.scale_log2 < 0.0f ? -1.0f : 1.0f);
-        sl2 = fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + e) << 23), 1e-37f);
-        for (int i = 0; i < D / 8; ++i) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (real) x = reinterpret_cast<const uint4*>(src)[i];
-            uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int z = 0; z < 4; ++z) w[z] = pack_h2(lo16<BF>(w[z]) * f, hi16<BF>(w[z]) * f);
-            *reinterpret_cast<uint4*>(smem + L::q + (i / 8) * (kRows * 128) + row * 128 + ((i % 8 ^ (row & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        fence_proxy_async();
     }
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = *tmem_at;
 
-    float m = -INFINITY, l = 0.0f;
     if (warp < 8) {
         regs_up<kRegSoft>();
+        // queries: a thread a row, its power of two kept for the scores
+        const int row = threadIdx.x;  // of the block
+        const int r = r0 + row;
+        uint4 in[D / 8] = {};
+        if (r < rw.R) {
+            const uint16_t* src = a.q + (int64_t)(rw.c0 + r / G) * a.qs + (h * G + r % G) * D;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) in[i] = reinterpret_cast<const uint4*>(src)[i];
+        }
+        int e = 0;
+        if (BF) {
+            uint32_t mx = 0;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(in[i].x & 0x7fff7fffu, in[i].y & 0x7fff7fffu), __vmaxu2(in[i].z & 0x7fff7fffu, in[i].w & 0x7fff7fffu)));
+            const int eb = (int)(max(mx & 0xffffu, mx >> 16) >> 7);
+            if (eb < 255) e = max(eb - 127 - 10, -120);
+        }
+        // a negative scale goes into the query, so that the largest score is the largest product
+        const float f = __uint_as_float((uint32_t)(127 - e) << 23) * (a.scale_log2 < 0.0f ? -1.0f : 1.0f);
+        const float sl2 = fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + e) << 23), 1e-37f);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z) w[z] = pack_h2(lo16<BF>(w[z]) * f, hi16<BF>(w[z]) * f);
+            *reinterpret_cast<uint4*>(smem + L::q + (i / 8) * (kRows * 128) + row * 128 + ((i % 8 ^ (row & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        float m = -INFINITY, l = 0.0f;
         const int i = warp >> 2;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, in bits 16 and up
         const uint32_t st = tmem + lanes + i * 128, ot = tmem + lanes + 256 + i * D;
@@ -332,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
             }
             // a row that saw nothing has P = 0 times finite values: O = 0 exactly
             if (!real) continue;
-            if (a.S == 1) {
+            if (S == 1) {
 #pragma unroll
                 for (int z = 0; z < 32; z += 8) {
                     uint32_t w[4];
@@ -348,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
             }
         }
         if (real) {
-            if (a.S > 1) a.pml[s * nrow + grow] = make_float2(m, l);
+            if (S > 1) a.pml[s * nrow + grow] = make_float2(m, l);
             else if (a.lse) a.lse[grow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
         fence_before();
@@ -450,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
                 for (int k = 4 * half; k < 4 * half + 4; ++k)
                     mma_ts(tmem + 256 + i * D, tmem + i * 128 + k * 8, vi + k * (2048 / 16), io, add || k > 0);
             };
-            bool ok = n > 0 && wait_on(&kv_full[0], 0, dead);
+            bool ok = n > 0 && wait_on(q_full, 0, dead) && wait_on(&kv_full[0], 0, dead);
             if (ok) {
                 fence_after();
                 for (int i = 0; i < nact; ++i) scores(i, 0);
@@ -492,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a, i
 }
 
 template <int D, bool BF>
-int launch(const AttnArgs& a, int nrb, int B, cudaStream_t st) {
+int launch(const AttnArgs& a, cudaStream_t st) {
     auto* kern = k_paged_chunk<D, BF>;
     constexpr int smem = Smem<D>::total;
     static_assert(smem <= 232448, "shared memory of a block");
@@ -504,15 +510,16 @@ int launch(const AttnArgs& a, int nrb, int B, cudaStream_t st) {
         return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
     }();
     if (regs * 4 < 2 * kRegSoft + kRegDeq + kRegIssue) return KVQ_ERR_UNSUPPORTED;
-    return launch_overlapped(kern, dim3((unsigned)(a.S * nrb), a.c.Hkv, B), kThreads, smem, 1, st, a, nrb);
+    const int units = a.B * a.c.Hkv * a.nrb;
+    return launch_overlapped(kern, dim3((unsigned)(a.whole + (units - a.whole) * a.S)), kThreads, smem, 1, st, a);
 }
 
 }  // namespace
 
 namespace kvq_host {
-int run_chunk(const AttnArgs& a, int nrb, int B, cudaStream_t st) {
+int run_chunk(const AttnArgs& a, cudaStream_t st) {
     const bool bf = a.c.dtype == KVQ_BF16;
-    if (a.c.D == 64) return bf ? launch<64, true>(a, nrb, B, st) : launch<64, false>(a, nrb, B, st);
-    return bf ? launch<128, true>(a, nrb, B, st) : launch<128, false>(a, nrb, B, st);
+    if (a.c.D == 64) return bf ? launch<64, true>(a, st) : launch<64, false>(a, st);
+    return bf ? launch<128, true>(a, st) : launch<128, false>(a, st);
 }
 }  // namespace kvq_host

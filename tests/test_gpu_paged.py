@@ -271,6 +271,10 @@ CASES = [
     ("bf16", 128, 64, 2, 4, [6000, 1, 900], [1, 1, 1], 0, 0),
     ("fp16", 64, 32, 1, 2, [9000, 40, 0, 2500], [8, 8, 8, 5], 0, 0),
     ("bf16", 64, 128, 1, 4, [4000, 130], [33, 20], 0, 0),
+    # a wave of whole row blocks and a few that are split
+    ("bf16", 64, 16, 8, 3, [2900 - 37 * b for b in range(19)], [6 - b % 2 for b in range(19)], 0, 0),
+    ("fp16", 64, 32, 8, 8, [1500 - 29 * b for b in range(10)], [40 - b for b in range(10)], 0, 0),
+    ("bf16", 128, 64, 8, 3, [2900 - 37 * b for b in range(19)], [6] * 19, 1500, 0),
     # more requests than lanes, and than threads of a block; empty ones among them
     ("bf16", 128, 16, 1, 2, [(b * 37) % 190 for b in range(40)], [b % 3 for b in range(40)], 0, 0),
     ("fp16", 64, 16, 2, 1, [(b * 37) % 190 for b in range(300)], [(b + 1) % 2 for b in range(300)], 0, 2),
