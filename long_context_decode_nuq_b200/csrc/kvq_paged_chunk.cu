@@ -23,6 +23,13 @@ namespace {
 // with its row's power of two taken out, P rounded to fp16 at 2^12 .. 2^15 of its row's largest.
 // Products of one block run in the order they are issued, which is what lets S_i of the next
 // tokens be issued behind the product that still reads P_i from the same columns.
+//
+// Bound by the round trip between products and softmax: a step takes about 3700 cycles, 2048 of
+// them products; without the exponentials it would be 5 % less, without the conversions 11 %.
+// 2048 queries against 32768 tokens, 32/8 heads of 128: 933-980 us, 1.1-1.14 PFLOP/s (69 % of a
+// measured library product's rate).  Sixteen softmax warps of half a row each were slower (1187
+// against 1083 us), as were P in quarters (1061 against 1015) and part of the exponentials on the
+// multiply-add pipe (1034 against 1017).
 constexpr int kRows = kChunkRows;   // 2 tiles of 128
 constexpr int kTok = 128;           // tokens a step
 constexpr int kSlots = 4;           // K or V tiles in shared memory

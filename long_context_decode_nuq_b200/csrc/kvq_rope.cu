@@ -10,7 +10,8 @@ namespace {
 // [-pi, pi] there (a position of a million leaves no digits to a binary32 product), cos and sin of
 // the remainder in binary32, once per (token, pair) into shared memory.  Then a thread keeps the 8
 // (cos, sin) of its 8 pairs in registers and turns them for one head after the other, two (four
-// for binary32) 16-byte loads and stores each.  HBM bound: each value read and written once.
+// for binary32) 16-byte loads and stores each.  HBM bound, each value read and written once: 32768
+// tokens of 40 heads of 128 in bf16 take 112-114 us, 5.9 TB/s (90 % of the measured copy rate).
 constexpr int kRopeThreads = 256;
 
 struct RopeArgs {
