@@ -26,8 +26,8 @@ namespace {
 //
 // Bound by the round trip between products and softmax: a step takes about 3700 cycles, 2048 of
 // them products; without the exponentials it would be 5 % less, without the conversions 11 %.
-// 2048 queries against 32768 tokens, 32/8 heads of 128: 933-980 us, 1.1-1.14 PFLOP/s (69 % of a
-// measured library product's rate).  Sixteen softmax warps of half a row each were slower (1187
+// 2048 queries against 32768 tokens, 32/8 heads of 128: 933 us in short runs, 1022 in long ones at
+// the power limit, 1.14 and 1.04 PFLOP/s (69 and 63 % of a measured library product's rate).  Sixteen softmax warps of half a row each were slower (1187
 // against 1083 us), as were P in quarters (1061 against 1015) and part of the exponentials on the
 // multiply-add pipe (1034 against 1017).
 constexpr int kRows = kChunkRows;   // 2 tiles of 128
