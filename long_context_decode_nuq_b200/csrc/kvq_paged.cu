@@ -302,9 +302,11 @@ __device__ __forceinline__ bool slot_ok(int slot, int limit, int32_t* status) {
 // amax / 6 is amax * rn(1/6), and y / s is q = y r with r near 1/s and one residual step,
 // q + (y - q s) r: both land on the same side of every decision point as the quotients do, and on
 // the point itself when the quotient is one (checked over every 11-bit significand and every
-// scale; without the residual step 60 quotients miss).
+// scale; without the residual step 60 quotients miss).  Where y r may pass binary32 the residual
+// would be inf - inf, so values from `past` on, which lie beyond 6 times the largest scale, are
+// brought down to 7 times it first.
 template <bool BF>
-__device__ __forceinline__ uint2 quantize16(const uint4 (&w4)[2], float down, float up, uint32_t* scale) {
+__device__ __forceinline__ uint2 quantize16(const uint4 (&w4)[2], float down, float up, uint32_t past, uint32_t* scale) {
     const uint32_t w[8] = {w4[0].x, w4[0].y, w4[0].z, w4[0].w, w4[1].x, w4[1].y, w4[1].z, w4[1].w};
     // |x| of a 16-bit float orders as its bits, NaNs above infinity
     uint32_t mx = 0;
@@ -315,13 +317,14 @@ __device__ __forceinline__ uint2 quantize16(const uint4 (&w4)[2], float down, fl
 #pragma unroll
     for (int q = 0; q < 8; ++q) x[2 * q] = lo16<BF>(w[q]), x[2 * q + 1] = hi16<BF>(w[q]);
     float am = lo16<BF>(mx);
-    if (mx >= (BF ? 0x7f80u : 0x7c00u)) {  // infinities or NaNs among them
+    if (mx >= past) {  // values far past the largest scale, infinities or NaNs among them
         am = 0.0f;
+        const float top = 7.0f * 448.0f * up;  // stored as 6 * 448 * up, like all beyond; x r stays finite
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
             if (x[q] != x[q]) x[q] = 0.0f;
             am = fmaxf(am, fabsf(x[q]));
-            x[q] = fminf(fmaxf(x[q], -1e30f), 1e30f);
+            x[q] = fminf(fmaxf(x[q], -top), top);
         }
     }
     uint16_t sb;
@@ -366,6 +369,8 @@ __global__ void __launch_bounds__(kAppThreads)
     const int64_t stride = val ? vs : ks;
     const int e = val ? cfg.v_exp : cfg.k_exp, lp = 31 - __clz(cfg.page_tokens), limit = cfg.num_pages << lp;
     const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+    // the type's bits of 2^(e + 12), or of infinity; 0 where that is no normal number
+    const uint32_t past = BF ? min(max(127 + e + 12, 0), 255) << 7 : min(max(15 + e + 12, 0), 31) << 10;
     for (int i = w.i0; i < w.i1; i += kAhead * w.step) {
         uint4 x[kAhead][2];
         int slot[kAhead];
@@ -382,7 +387,7 @@ __global__ void __launch_bounds__(kAppThreads)
         for (int z = 0; z < kAhead; ++z) {
             if (!slot_ok(slot[z], limit, status)) continue;
             uint32_t sb;
-            const uint2 code = quantize16<BF>(x[z], down, up, &sb);
+            const uint2 code = quantize16<BF>(x[z], down, up, past, &sb);
             uint8_t* g = pool + row_at<D>(cfg, slot[z], lp) + w.at;
             *reinterpret_cast<uint2*>(g) = code;
             g[scale_off<D, 16>(slot[z], w.r)] = (uint8_t)sb;
