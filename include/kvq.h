@@ -545,8 +545,10 @@ int kvq_page_plan(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_
 /*
  * Give back the pages of finished requests: for each b with done[b] != 0, in request order, its
  * ceil(len[b]/P) pages go on top of the free list in table order, their table entries become -1
- * and len[b] becomes 0.  n_free is updated in place.  Pages that would pass num_pages entries are
- * dropped and set KVQ_STATUS_BAD_PAGE.  A page that stands in two tables would be given back
+ * and len[b] becomes 0.  An entry of -1 is left out: a page behind a window may be given back early,
+ * its entry cleared and its number put on the list by the caller.  So is any other number outside
+ * the pool, with KVQ_STATUS_BAD_PAGE.  n_free is updated in place.  Pages that would pass num_pages
+ * entries are dropped and set KVQ_STATUS_BAD_PAGE.  A page that stands in two tables would be given back
  * twice: while requests share one, who may release it is the caller's to count.
  *   free_pages   int32 [num_pages]
  */

@@ -207,18 +207,23 @@ int launch_plan(const PlanArgs& a, int blocks, int threads, cudaStream_t st) {
     return launch_overlapped(k_page_plan<ITEMS>, dim3(blocks), threads, smem, blocks, st, a);
 }
 
-// Release: the same walk over requests, one block; pages pushed in request order.  Latency bound: a
-// handful of requests end in a step.
+// Release: the same walk over requests, one block; pages pushed in request order, 1024 entries at a
+// time with their places counted by ballots, as an entry may be no page.  Latency bound: a handful of
+// requests end in a step.  One of 130 pages takes 2.9 us in a graph of calls, 64 of
+// 512 at once 28.
 __global__ void __launch_bounds__(kPlanThreads)
     k_page_release(int B, int P, int num_pages, int max_pages, int32_t* len, const int32_t* done,
                    int32_t* table, int32_t* free_pages, int32_t* n_free_p, int32_t* status) {
     __shared__ uint32_t s_page[kPlanThreads];
     __shared__ long long s_scan[2][32];
-    const int tid = threadIdx.x, nt = blockDim.x;
+    __shared__ int s_count[2][kPlanThreads / 32];
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
     let_next();
     after_previous();
     const int n_free = min(max(*n_free_p, 0), num_pages);
-    long long page0 = 0;
+    long long pushed = 0;
+    bool bad = false;
+    int turn = 0;
     for (int base = 0; base < B; base += nt) {
         const int b = base + tid, m = min(nt, B - base);
         long long cnt = 0, zero = 0, tc, tz;
@@ -230,20 +235,40 @@ __global__ void __launch_bounds__(kPlanThreads)
         scan2(c, zero, s_scan, &tc, &tz);
         s_page[tid] = (uint32_t)min(c - cnt, (long long)UINT32_MAX);
         __syncthreads();
-        for (long long r = tid; r < tc; r += nt) {
-            const int j = find_last(s_page, m, (uint32_t)r);
-            int32_t* e = table + (size_t)(base + j) * max_pages + (int)(r - s_page[j]);
-            const long long at = n_free + page0 + r;
-            if (at < num_pages) free_pages[at] = *e;
-            *e = -1;
+        int32_t* e = nullptr;
+        int page = -1;
+        auto fetch = [&](long long r) {  // entry r of the chunk's
+            e = nullptr, page = -1;
+            if (r < tc) {
+                const int j = find_last(s_page, m, (uint32_t)r);
+                e = table + (size_t)(base + j) * max_pages + (int)(r - s_page[j]);
+                page = *e;
+            }
+        };
+        fetch(tid);
+        for (long long r0 = 0; r0 < tc; r0 += nt, turn ^= 1) {
+            int32_t* const at_e = e;
+            const int p = page;
+            if (r0 + nt < tc) fetch(r0 + nt + tid);  // to come while these are counted
+            if (at_e) *at_e = -1;
+            const bool ok = p >= 0 && p < num_pages;
+            bad |= !ok && p != -1;
+            const uint32_t oks = __ballot_sync(0xffffffffu, ok);
+            if (lane == 0) s_count[turn][warp] = __popc(oks);
+            __syncthreads();
+            const int count = s_count[turn][lane];  // 32 warps
+            const long long at = n_free + pushed + __reduce_add_sync(0xffffffffu, lane < warp ? count : 0) +
+                                 __popc(oks & ((1u << lane) - 1u));
+            if (ok && at < num_pages) free_pages[at] = p;
+            pushed += __reduce_add_sync(0xffffffffu, count);
         }
-        page0 += tc;
         __syncthreads();
     }
     if (tid == 0) {
-        if (n_free + page0 > num_pages) atomicOr(status, KVQ_STATUS_BAD_PAGE);
-        *n_free_p = (int32_t)min(n_free + page0, (long long)num_pages);
+        bad |= n_free + pushed > num_pages;
+        *n_free_p = (int32_t)min(n_free + pushed, (long long)num_pages);
     }
+    if (bad) atomicOr(status, KVQ_STATUS_BAD_PAGE);
 }
 
 // ---------------------------------------------------------------------------------

@@ -36,3 +36,51 @@ def test_append_values_far_past_the_largest_scale(dtype, exp):
     K.kvq_paged_dequantize(K.PagedCache(K.make_paged_cfg(1, 1, 128, 16, 4, 4, DT[dtype]), pool=c.pool), slots, kh, vh)
     assert torch.equal(kh.cpu(), want) and torch.equal(vh.cpu(), want)
     assert K.kvq_paged_get_status(c) == 0
+
+
+# ------------------------------------------------------------------------------ pages
+@pytest.mark.parametrize("P", [16, 128])
+@pytest.mark.parametrize("B,width", [(3, 9), (40, 60), (1500, 5)])
+def test_release_of_tables_whose_first_pages_are_gone(P, B, width):
+    """Pages behind a window that were given back early have entries of -1: release leaves those
+    out, and every page is on the list exactly once."""
+    r = np.random.RandomState(B)
+    lens = r.randint(0, width * P + 1, B)
+    need = -(-lens // P)
+    pages = int(need.sum()) + 3
+    c = K.PagedCache(K.make_paged_cfg(1, 1, 64, P, pages, width, torch.bfloat16))
+    perm, table, at = r.permutation(pages), np.full((B, width), -1), 0
+    early, late, ended = [], [], r.rand(B) < 0.7
+    ended[0] = True
+    for b in range(B):
+        own, gone = perm[at:at + need[b]], r.randint(0, need[b] + 1)
+        at += need[b]
+        table[b, gone:need[b]] = own[gone:]
+        early += own[:gone].tolist()
+        if ended[b]:
+            late += own[gone:].tolist()
+    first = perm[at:].tolist() + early  # the list while the requests run
+    free = np.full(pages, -9)
+    free[:len(first)] = first
+    d_lens, d_table, d_free, n_free = i32(lens), i32(table), i32(free), i32([len(first)])
+    K.kvq_page_release(c, d_lens, i32(ended), d_table, d_free, n_free)
+    assert K.kvq_paged_get_status(c) == 0
+    assert d_free.tolist()[:int(n_free)] == first + late
+    assert d_lens.tolist() == np.where(ended, 0, lens).tolist()
+    assert np.array_equal(d_table.cpu().numpy(), np.where(ended[:, None], -1, table))
+    # what the plan hands out next is a page
+    n_new = i32([0] * (B - 1) + [P]) if ended[-1] else i32([P] + [0] * (B - 1))
+    slots, pos = i32([0] * P), i32([0] * P)
+    if int(n_free):
+        K.kvq_page_plan(c, d_lens, n_new, d_table, d_free, n_free, i32([0] * (B + 1)), d_lens, n_free, slots, pos)
+        assert K.kvq_paged_get_status(c) == 0 and bool((slots >= 0).all())
+
+
+def test_release_reports_entries_outside_the_pool():
+    c = K.PagedCache(K.make_paged_cfg(1, 1, 64, 16, 6, 4, torch.bfloat16))
+    lens, table, free, n_free = i32([64, 33]), i32([[2, 6, -1, 0], [-1, 4, 5, -1]]), i32([1, 0, 0, 0, 0, 0]), i32([1])
+    K.kvq_page_release(c, lens, i32([0, 1]), table, free, n_free)
+    assert free.tolist()[:3] == [1, 4, 5] and int(n_free) == 3 and K.kvq_paged_get_status(c) == 0
+    K.kvq_page_release(c, lens, i32([1, 1]), table, free, n_free)
+    assert free.tolist()[:5] == [1, 4, 5, 2, 0] and int(n_free) == 5 and K.kvq_paged_get_status(c) == K.KVQ_STATUS_BAD_PAGE
+    assert bool((table == -1).all()) and not lens.any()
