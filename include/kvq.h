@@ -604,7 +604,10 @@ int kvq_paged_attention(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, 
                         int32_t max_len, float sm_scale, int32_t window, void* out, float* lse,
                         void* workspace, size_t workspace_bytes, int32_t splits, void* stream);
 
-/* Workspace bytes of kvq_paged_attention for the same sizes. */
+/* Workspace bytes of kvq_paged_attention for the same sizes, whatever the window.  With splits = 0
+ * also enough for every call of the configuration with splits = 0 and no size larger; then at most
+ * 888 * 256 rows of (D + 2) floats (118 MB at D = 128) where max_len is at most 2^17, and a part of
+ * every query row for each 2^17 tokens beyond. */
 int kvq_paged_attention_workspace(const kvq_paged_cfg* cfg, int32_t B, int32_t total_q,
                                   int32_t max_q, int32_t max_len, int32_t splits, size_t* bytes);
 

@@ -662,26 +662,27 @@ constexpr int kMergeWarps = 4;
 template <int D, bool BF>
 __global__ void __launch_bounds__(kMergeWarps * 32) k_paged_merge(const AttnArgs a) {
     constexpr int PB = kChunkRows / kMergeWarps;  // blocks of a unit
-    const Unit unit = unit_of(a, a.whole + (int)blockIdx.x / PB);
+    const int cut = (int)blockIdx.x / PB, r0 = (int)blockIdx.x % PB * kMergeWarps + (threadIdx.x >> 5);
+    const Unit unit = unit_of(a, a.whole + cut);
     const int h = unit.h, b = unit.b, lane = threadIdx.x & 31;
     const int G = a.c.Hq / a.c.Hkv;
     let_next();
     after_previous();
     const Rows rw = rows_of(a, b);
-    const int64_t nrow = (int64_t)a.total_q * a.c.Hq;
-    const int r = unit.rb * kChunkRows + (int)blockIdx.x % PB * kMergeWarps + (threadIdx.x >> 5);
+    const int r = unit.rb * kChunkRows + r0;
     if (r >= rw.R) return;
     const int64_t grow = (int64_t)(rw.c0 + r / G) * a.c.Hq + h * G + r % G;
+    const int64_t at = part_at(a, 0, cut, r0, grow);
     float M = -INFINITY;
-    for (int s = lane; s < a.S; s += 32) M = fmaxf(M, a.pml[s * nrow + grow].x);
+    for (int s = lane; s < a.S; s += 32) M = fmaxf(M, a.pml[s * a.part_rows + at].x);
 #pragma unroll
     for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
     float L = 0.0f, acc[D / 32] = {};
     for (int s = 0; s < a.S; ++s) {
-        const float2 ml = a.pml[s * nrow + grow];
+        const float2 ml = a.pml[s * a.part_rows + at];
         if (ml.y == 0.0f) continue;  // an empty split; one of NaN scores has m = -inf, l = NaN
         const float f = ex2(ml.x - M);
-        const float* x = a.part + (s * nrow + grow) * D + lane * (D / 32);
+        const float* x = a.part + (s * a.part_rows + at) * D + lane * (D / 32);
         L += f * ml.y;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) acc[i] += f * x[i];
@@ -701,6 +702,8 @@ struct Plan {
     int nrb;  // chunk kernel: row blocks
     int64_t units, whole;  // chunk kernel: row blocks of all (request, kv head)s; those not split
     int S;    // chunk kernel: splits of the other units;  k_paged_attn: blocks, or blocks of a cluster
+    int64_t part_rows;  // chunk kernel: rows of a split's parts,
+    bool by_unit;       // the split units' (true) or all of q's, whichever are fewer
     bool cluster;
     bool join;
 };
@@ -709,32 +712,39 @@ constexpr int kSms = 148;
 // More rows of a kv head than this go to the chunk kernel.
 constexpr int kFewRows = 16;
 
-// How the chunk kernel's units (256 rows of a kv head each) are spread: the first `whole` get a
-// block each, the others S, whose parts k_paged_merge adds.  The least time of a model in which a
-// block costs 10 us and 2 us per 128 tokens (measured: 2.0), blocks run one per SM in waves, and a
-// split writes and reads its part at 5 TB/s; whole units come in full waves.  Against 32768 tokens,
-// 8 kv heads: 64 queries 514 us in one part, 59 in 18; 1184 queries (152 units) 728 us all whole,
-// 560 with the last 4 split.
-void chunk_splits(const kvq_paged_cfg* c, int64_t units, int64_t tiles, int64_t* whole, int* splits) {
-    *whole = units, *splits = 1;
-    const int64_t waves = units / kSms;
-    double least = (double)((units + kSms - 1) / kSms) * (10.0 + 2.0 * (double)tiles);
-    for (int64_t w = waves; w >= 0; w = w == 0 ? -1 : w == waves ? w - 1 : 0)  // all full waves whole, one less, none
-        for (int S = 2; S <= kSms && S <= tiles; ++S) {
-            const int64_t rest = units - w * kSms;
-            if (rest == 0) break;
-            const double t = (double)w * (10.0 + 2.0 * (double)tiles) + 4.0 + (double)rest * S * kChunkRows * c->D * 8 / 5e6 +
-                             (double)((rest * S + kSms - 1) / kSms) * (10.0 + 2.0 * (double)((tiles + S - 1) / S));
-            if (t < 0.98 * least) least = t, *whole = w * kSms, *splits = S;
-        }
-}
-
 // Most tokens of a split of the chunk kernel.  The tensor cores cut their binary32 sums off instead
 // of rounding them, so O drifts toward 0 with every 16 tokens added: by 8e-4 of itself over 2^20
 // tokens of like sign (measured), by 1e-4, a fifth of fp16's half step, over 2^17.
 constexpr int kSplitTokens = 1 << 17;
 
-Plan plan_of(const kvq_paged_cfg* c, int B, int max_q, int max_len, int splits, int window) {
+// Blocks of split units by the library's choice, at most: it is what bounds the workspace, and
+// the model below asks for more only beyond 2^17 tokens (up to 5000 units).
+constexpr int64_t kCutBlocks = 6 * kSms;
+
+int64_t least_splits(int64_t span) { return (span + kSplitTokens - 1) / kSplitTokens; }
+
+// How the chunk kernel's units (256 rows of a kv head each) are spread: the first `whole` get a
+// block each, the others S, whose parts k_paged_merge adds.  The least time of a model in which a
+// block costs 10 us and 2 us per 128 tokens (measured: 2.0), blocks run one per SM in waves, and a
+// split writes and reads its part at 5 TB/s; whole units come in full waves, and there are none
+// where a split must not have all tokens.  Against 32768 tokens, 8 kv heads: 64 queries 514 us in
+// one part, 59 in 18; 1184 queries (152 units) 728 us all whole, 560 with the last 4 split.
+void chunk_splits(const kvq_paged_cfg* c, int64_t units, int64_t span, int64_t* whole, int* splits) {
+    const int64_t tiles = (span + 127) / 128, must = least_splits(span);
+    const int64_t waves = must > 1 ? 0 : units / kSms, most = must > kSms ? must : kSms;
+    *whole = must > 1 ? 0 : units, *splits = (int)must;
+    double least = must > 1 ? 1e30 : (double)((units + kSms - 1) / kSms) * (10.0 + 2.0 * (double)tiles);
+    for (int64_t w = waves; w >= 0; w = w == 0 ? -1 : w == waves ? w - 1 : 0)  // all full waves whole, one less, none
+        for (int64_t S = must > 1 ? must : 2; S <= most && S <= tiles; ++S) {
+            const int64_t rest = units - w * kSms;
+            if (rest == 0 || (S > must && rest * S > kCutBlocks)) break;
+            const double t = (double)w * (10.0 + 2.0 * (double)tiles) + 4.0 + (double)rest * S * kChunkRows * c->D * 8 / 5e6 +
+                             (double)((rest * S + kSms - 1) / kSms) * (10.0 + 2.0 * (double)((tiles + S - 1) / S));
+            if (t < 0.98 * least) least = t, *whole = w * kSms, *splits = (int)S;
+        }
+}
+
+Plan plan_of(const kvq_paged_cfg* c, int B, int total_q, int max_q, int max_len, int splits, int window) {
     const int64_t R = (int64_t)max_q * (c->Hq / c->Hkv);
     // no row block sees more tokens than this
     int64_t span = max_len;
@@ -744,21 +754,17 @@ Plan plan_of(const kvq_paged_cfg* c, int B, int max_q, int max_len, int splits, 
     p.nrb = p.nt ? 1 : (int)((R + kChunkRows - 1) / kChunkRows);
     const int64_t units = p.units = (int64_t)B * c->Hkv * p.nrb;
     if (p.nt == 0) {
-        p.whole = 0, p.S = splits;
-        if (!splits) {
-            chunk_splits(c, units, (span + 127) / 128, &p.whole, &p.S);
-            // the workspace is sized without the window, which must not raise the splits
-            int64_t whole;
-            int S = p.S;
-            if (span < max_len) chunk_splits(c, units, ((int64_t)max_len + 127) / 128, &whole, &S);
-            if (S < p.S) p.S = S;
+        if (splits) {
+            const int64_t least = least_splits(span);
+            p.whole = 0, p.S = (int)(splits < least ? least : splits);
+            if (p.S == 1) p.whole = units;
+        } else {
+            chunk_splits(c, units, span, &p.whole, &p.S);
         }
-        if (span > kSplitTokens) {
-            const int64_t least = (span + kSplitTokens - 1) / kSplitTokens;
-            p.whole = 0, p.S = (int)(p.S < least ? least : p.S);
-        }
-        if (p.S == 1) p.whole = units;
         p.join = p.S > 1;
+        const int64_t by_unit = (units - p.whole) * kChunkRows, by_row = (int64_t)total_q * c->Hq;
+        p.by_unit = by_unit < by_row;
+        p.part_rows = p.by_unit ? by_unit : by_row;
         return p;
     }
     p.cluster = false;
@@ -789,10 +795,35 @@ int64_t records(const kvq_paged_cfg* cfg, const Plan& p, int32_t B) {
     return segs < p.S ? segs : p.S;
 }
 
-size_t ws_bytes(const kvq_paged_cfg* cfg, const Plan& p, int32_t B, int32_t total_q) {
+// What a call needs.
+size_t ws_bytes(const kvq_paged_cfg* cfg, const Plan& p, int32_t B) {
     if (!p.join) return 0;
-    if (p.nt == 0) return (size_t)p.S * total_q * cfg->Hq * (cfg->D + 2) * 4;
+    if (p.nt == 0) return (size_t)p.S * p.part_rows * (cfg->D + 2) * 4;
     return (size_t)(2 * p.S) * 8 * p.nt * (cfg->D + 2) * 4 + (size_t)records(cfg, p, B) * 16;
+}
+
+// What the query answers: what the call needs or, for chunks by the library's choice, a bound that
+// grows with every size, so that it also serves whatever is smaller (a few rows' calls among it;
+// those grow with the sizes by themselves).  A split unit's blocks number kCutBlocks at most, or
+// the least that the tokens ask for.
+size_t ws_query(const kvq_paged_cfg* cfg, int B, int total_q, int max_q, int max_len, int splits) {
+    const Plan p = plan_of(cfg, B, total_q, max_q, max_len, splits, 0);
+    if (p.nt || splits) return ws_bytes(cfg, p, B);
+    const int64_t by_unit = p.units * kChunkRows, by_row = (int64_t)total_q * cfg->Hq;
+    const int64_t tiles = ((int64_t)max_len + 127) / 128, most = tiles < kSms ? tiles : kSms;
+    const int64_t all = by_unit < by_row ? by_unit : by_row;
+    int64_t rows = kCutBlocks * kChunkRows;
+    if (most < 2) rows = 0;
+    else if (all < rows && all * most < rows) rows = all * most;
+    const int64_t least = least_splits(max_len);
+    if (least > 1 && all * least > rows) rows = all * least;
+    size_t bytes = (size_t)rows * (cfg->D + 2) * 4;
+    const int G = cfg->Hq / cfg->Hkv;
+    if (G <= kFewRows) {
+        const size_t few = ws_bytes(cfg, plan_of(cfg, B, total_q, kFewRows / G, max_len, 0, 0), B);
+        if (few > bytes) bytes = few;
+    }
+    return bytes;
 }
 
 // Few rows: the main kernel, and the join where a (request, kv head) may have been cut.
@@ -831,7 +862,7 @@ int kvq_paged_attention_workspace(const kvq_paged_cfg* cfg, int32_t B, int32_t t
     if (e) return e;
     if (!bytes) return KVQ_ERR_NULL;
     if ((e = check_sizes(cfg, B, total_q, max_q, max_len, splits))) return e;
-    *bytes = ws_bytes(cfg, plan_of(cfg, B, max_q, max_len, splits, 0), B, total_q);
+    *bytes = ws_query(cfg, B, total_q, max_q, max_len, splits);
     return KVQ_OK;
 }
 
@@ -851,11 +882,11 @@ int kvq_paged_attention(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, 
     if (!q || !len || !block_table || !out) return KVQ_ERR_NULL;
     if (!aligned16(q) || !aligned16(out) || (q_stride & 7)) return KVQ_ERR_ALIGN;
     if (q_stride < (int64_t)cfg->Hq * cfg->D) return KVQ_ERR_SHAPE;
-    const Plan p = plan_of(cfg, B, max_q, max_len, splits, window);
+    const Plan p = plan_of(cfg, B, total_q, max_q, max_len, splits, window);
     // blocks of the chunk kernel and of its merge
     const int64_t per_unit = !p.join ? 1 : p.S > kChunkRows / kMergeWarps ? p.S : kChunkRows / kMergeWarps;
     if (p.nt == 0 && p.units * per_unit > INT32_MAX) return KVQ_ERR_RANGE;
-    const size_t need = ws_bytes(cfg, p, B, total_q);
+    const size_t need = ws_bytes(cfg, p, B);
     if (need > 0) {
         if (!workspace) return KVQ_ERR_NULL;
         if (!aligned16(workspace)) return KVQ_ERR_ALIGN;
@@ -871,7 +902,7 @@ int kvq_paged_attention(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, 
     a.out = (uint16_t*)out;
     a.lse = lse;
     a.part = (float*)workspace;
-    const size_t prow = p.nt ? (size_t)2 * p.S * 8 * p.nt : (size_t)p.S * total_q * cfg->Hq;
+    const size_t prow = p.nt ? (size_t)2 * p.S * 8 * p.nt : (size_t)p.S * p.part_rows;
     if (p.join) {
         a.pml = (float2*)(a.part + prow * cfg->D);
         if (p.nt) {
@@ -886,6 +917,7 @@ int kvq_paged_attention(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, 
     cudaStream_t st = (cudaStream_t)stream;
     if (p.nt == 0) {
         a.whole = (int)p.whole, a.B = B, a.nrb = p.nrb;
+        a.part_rows = p.part_rows, a.by_unit = p.by_unit;
         if ((e = run_chunk(a, st))) return e;
         if (p.join) {
             auto* mk = cfg->D == 64 ? (bf ? k_paged_merge<64, true> : k_paged_merge<64, false>)

@@ -25,6 +25,8 @@ struct AttnArgs {
     int32_t S;         // splits (chunk kernel, of the units behind the whole ones); blocks of a cluster
     int32_t whole;     // chunk kernel: units that one block does alone
     int32_t B, nrb;    // chunk kernel: requests, row blocks of a (request, kv head)
+    int64_t part_rows; // chunk kernel: rows of a split's parts: those of the split units, or all of q's
+    bool by_unit;      // (the former, else the latter)
     float scale_log2, out_scale;
 };
 
@@ -57,6 +59,13 @@ __device__ __forceinline__ Unit unit_of(const AttnArgs& a, int u) {
     return {a.nrb - 1 - u / (a.B * a.c.Hkv), seg / a.c.Hkv, seg % a.c.Hkv};
 }
 
+// Chunk kernel and merge: where split s keeps its part of row r (of the unit) = grow (of q), unit
+// being the `cut`-th of those that are split.
+constexpr int kUnitRows = 256;
+__device__ __forceinline__ int64_t part_at(const AttnArgs& a, int s, int cut, int r, int64_t grow) {
+    return s * a.part_rows + (a.by_unit ? (int64_t)cut * kUnitRows + r : grow);
+}
+
 template <bool BF>
 __device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack16<BF>(a, b), pack16<BF>(c, d));
@@ -66,6 +75,6 @@ __device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, f
 
 namespace kvq_host {
 // Prompt chunks (kvq_paged_chunk.cu): query rows of a block, and the launch.
-constexpr int kChunkRows = 256;
+constexpr int kChunkRows = kvq::kUnitRows;
 int run_chunk(const kvq::AttnArgs& a, cudaStream_t stream);
 }  // namespace kvq_host

@@ -331,8 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a) {
             fence_after();
         }
         const bool real = i < nact && r < rw.R;
-        const int64_t nrow = (int64_t)a.total_q * a.c.Hq;
         const int64_t grow = (int64_t)(rw.c0 + r / G) * a.c.Hq + h * G + r % G;
+        const int64_t at = S > 1 ? part_at(a, s, cut / S, row, grow) : 0;
         const float inv = l == 0.0f ? 0.0f : a.out_scale / l;
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
@@ -357,11 +357,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_chunk(const AttnArgs a) {
             } else {
 #pragma unroll
                 for (int z = 0; z < 32; z += 4)
-                    *reinterpret_cast<uint4*>(a.part + (s * nrow + grow) * D + c + z) = make_uint4(o[z], o[z + 1], o[z + 2], o[z + 3]);
+                    *reinterpret_cast<uint4*>(a.part + at * D + c + z) = make_uint4(o[z], o[z + 1], o[z + 2], o[z + 3]);
             }
         }
         if (real) {
-            if (S > 1) a.pml[s * nrow + grow] = make_float2(m, l);
+            if (S > 1) a.pml[at] = make_float2(m, l);
             else if (a.lse) a.lse[grow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
         fence_before();
