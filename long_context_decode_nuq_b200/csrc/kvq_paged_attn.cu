@@ -721,6 +721,11 @@ constexpr int kSplitTokens = 1 << 17;
 // the model below asks for more only beyond 2^17 tokens (up to 5000 units).
 constexpr int64_t kCutBlocks = 6 * kSms;
 
+// Most tokens of one request that a warp of k_paged_attn adds up in a row, for the same reason: its
+// O drifts by 1.1e-7 for each 16 tokens, half of that on average over a growing sum, so by 1e-4 over
+// 2^15 (and by 3e-2 over 2^26 / 7, before there was a limit).
+constexpr int kWarpTokens = 1 << 15;
+
 int64_t least_splits(int64_t span) { return (span + kSplitTokens - 1) / kSplitTokens; }
 
 // How the chunk kernel's units (256 rows of a kv head each) are spread: the first `whole` get a
@@ -783,8 +788,10 @@ Plan plan_of(const kvq_paged_cfg* c, int B, int total_q, int max_q, int max_len,
     const int64_t most = units * per;
     int64_t N = splits ? units * splits : 2 * kSms;
     if (N > most) N = most;
+    const int64_t share = (int64_t)(p.nt == 1 ? kWarps<1> : kWarps<2>) * kWarpTokens;
+    if (per * kUnit > share && N < (most * kUnit + share - 1) / share) N = (most * kUnit + share - 1) / share;
     p.S = (int)(N > (1 << 20) ? 1 << 20 : N);
-    p.join = span > kUnit && !(splits == 1 && B == 1);
+    p.join = span > kUnit && !(splits == 1 && B == 1 && p.S == units);
     return p;
 }
 

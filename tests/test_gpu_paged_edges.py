@@ -84,3 +84,31 @@ def test_release_reports_entries_outside_the_pool():
     K.kvq_page_release(c, lens, i32([1, 1]), table, free, n_free)
     assert free.tolist()[:5] == [1, 4, 5, 2, 0] and int(n_free) == 5 and K.kvq_paged_get_status(c) == K.KVQ_STATUS_BAD_PAGE
     assert bool((table == -1).all()) and not lens.any()
+
+
+# ------------------------------------------------------------------------------ attention
+@pytest.mark.parametrize("B,Hkv,n,T,splits", [(1, 1, 1, 1 << 26, 1), (1, 1, 16, 1 << 26, 1), (5, 64, 1, 1 << 25, 0), (1, 1, 20, 1 << 26, 1), (1, 1, 1, 1 << 26, 0)])
+def test_attention_sums_do_not_drift(B, Hkv, n, T, splits):
+    """Equal weights over values of one sign, the same few pages again and again, so that the sums
+    only grow.  Tolerance: the output's half step, and 2^13 times in a row at most that a sum is cut
+    off, by less than a step (2^-23) of what has been summed by then: 2^13 / 2 * 2^-23 = 2^-11 of
+    the whole.  (Chunks: 2^17 tokens, 16 at a time.  Few rows: 2^15 tokens a warp, 16 at a time,
+    where an instruction may cut off up to four times.)  Parts are joined in binary32: 2^-24 for
+    each of up to 2^10, as the warps and blocks that join them add theirs in a tree."""
+    P, D, pages = 128, 64, 64
+    c = K.PagedCache(K.make_paged_cfg(Hkv, Hkv, D, P, pages, T // P, torch.float16))
+    v = torch.rand((pages * P, Hkv, D), generator=torch.Generator("cuda").manual_seed(1), device="cuda").half() + 0.5
+    slots = torch.arange(pages * P, dtype=torch.int32, device="cuda")
+    K.kvq_paged_append(c, torch.zeros_like(v), v, slots)
+    kh = torch.empty_like(v)
+    K.kvq_paged_dequantize(c, slots, kh, v)
+    want = v.double().mean(0)
+    table = (torch.arange(T // P, device="cuda") % pages).int().repeat(B, 1)
+    q = torch.randn((B * n, Hkv, D), device="cuda").half()
+    out = torch.empty_like(q)
+    ws = torch.empty(max(16, K.kvq_paged_attention_workspace(c.cfg, B, B * n, n, T, splits)), dtype=torch.uint8, device="cuda")
+    K.kvq_paged_attention(c, q, i32(range(0, B * n + 1, n)), i32([T] * B), table, n, T, 1.0, out, ws, splits=splits)
+    # the last query sees every page equally often
+    worst = ((out[n - 1::n].double() - want).abs() / want).max().item()
+    assert worst <= 2.0 ** -11 * 1.01 + 2.0 ** -11 + 2.0 ** -14, worst
+    assert K.kvq_paged_get_status(c) == 0
