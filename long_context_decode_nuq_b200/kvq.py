@@ -567,10 +567,11 @@ def kvq_paged_reset(cache: PagedCache, stream=None) -> None:
 
 def kvq_paged_get_status(cache: PagedCache, stream=None) -> int:
     out = c_int32()
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream(cache.device)
-    _check(load().kvq_paged_get_status(cache.args[1], byref(out), s.cuda_stream),
-           "kvq_paged_get_status")
+
+    def read(s):
+        return load().kvq_paged_get_status(cache.args[1], byref(out), s)
+
+    _call("kvq_paged_get_status", read, cache.index, stream)
     return out.value
 
 

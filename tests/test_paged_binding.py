@@ -1,0 +1,37 @@
+"""What the paged cache's binding does before and around the library's calls (no GPU)."""
+import contextlib
+
+import pytest
+import torch
+
+import long_context_decode_nuq_b200 as K
+from long_context_decode_nuq_b200 import kvq
+
+
+def test_status_is_read_on_the_caches_device(monkeypatch):
+    """A cache of device 3 while device 0 is current: the call runs on device 3 and its stream (the
+    default stream's handle is 0 on every device, and means the current one's)."""
+    c = K.PagedCache(K.make_paged_cfg(8, 2, 128, 16, 10, 4, torch.bfloat16), device="cpu")
+    c.index, c.device = 3, torch.device("cuda", 3)
+    current, seen = [0], []
+
+    @contextlib.contextmanager
+    def on(i):
+        old, current[0] = current[0], i
+        yield
+        current[0] = old
+
+    class Lib:
+        def kvq_paged_get_status(self, cache, out, stream):
+            seen.append((current[0], stream))
+            out._obj.value = 128
+            return 0
+
+    kvq._torch()
+    monkeypatch.setattr(kvq, "load", Lib)
+    monkeypatch.setattr(kvq, "_current", lambda: current[0])
+    monkeypatch.setattr(kvq, "_raw_stream", lambda i: 1000 + i)
+    monkeypatch.setattr(torch.cuda, "device", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: type("S", (), {"cuda_stream": 1000 + d.index}))
+    assert K.kvq_paged_get_status(c) == 128
+    assert seen == [(3, 1003)] and current[0] == 0
