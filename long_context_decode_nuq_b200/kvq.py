@@ -90,6 +90,7 @@ class PagedStruct(ctypes.Structure):
 class RopeCfg(ctypes.Structure):
     _fields_ = [(f, c_int32) for f in ("Hq", "Hkv", "D", "rot_dim", "dtype", "adjacent", "axes")]
     _fields_ += [("pair_axis", c_uint8 * 128)]
+    py = None  # kept by make_rope_cfg
 
 
 _lib = None
@@ -678,9 +679,17 @@ def make_rope_cfg(Hq, Hkv, D, rot_dim, pair_axis, dtype, adjacent=False) -> Rope
                          f"{rot_dim // 2} pairs")
     cfg = RopeCfg(Hq, Hkv, D, rot_dim, _dtype_code(dtype), int(bool(adjacent)), max(axes) + 1,
                   (c_uint8 * 128)(*axes))
-    _torch()
-    cfg.py = Hq, Hkv, D, max(axes) + 1, rot_dim // 2, dtype  # for kvq_rope's checks
+    cfg.py = _rope_shape(cfg)
     return cfg
+
+
+def _rope_shape(cfg: RopeCfg):
+    """What kvq_rope checks the tensors against."""
+    torch = _torch()
+    dtypes = torch.float16, torch.bfloat16, torch.float32
+    if not 0 <= cfg.dtype < len(dtypes):
+        raise ValueError(f"RopeCfg: dtype {cfg.dtype} is not float16, bfloat16 or float32's (0 .. 2)")
+    return cfg.Hq, cfg.Hkv, cfg.D, cfg.axes, cfg.rot_dim // 2, dtypes[cfg.dtype]
 
 
 def kvq_rope(cfg: RopeCfg, q, k, positions, freqs, q_out, k_out, inverse=False,
@@ -688,7 +697,7 @@ def kvq_rope(cfg: RopeCfg, q, k, positions, freqs, q_out, k_out, inverse=False,
     """q, k [n, heads, D] (k may be None when cfg.Hkv is 0), positions int32 [axes, n], freqs
     float64 [rot_dim / 2]; q_out and k_out may be q and k."""
     w, n, i = "kvq_rope", q.shape[0], q.get_device()
-    Hq, Hkv, d, axes, half, dtype = cfg.py
+    Hq, Hkv, d, axes, half, dtype = cfg.py or _rope_shape(cfg)
     _ints(w, i, positions)
     if positions.shape != (axes, n) and not (axes == 1 and positions.numel() == n):
         raise ValueError(f"{w}: positions is {tuple(positions.shape)}, not {(axes, n)}")

@@ -112,3 +112,15 @@ def test_attention_sums_do_not_drift(B, Hkv, n, T, splits):
     worst = ((out[n - 1::n].double() - want).abs() / want).max().item()
     assert worst <= 2.0 ** -11 * 1.01 + 2.0 ** -11 + 2.0 ** -14, worst
     assert K.kvq_paged_get_status(c) == 0
+
+
+# ------------------------------------------------------------------------------ together
+def test_rope_cfg_filled_by_hand():
+    x = torch.randn((5, 2, 64), device="cuda")
+    pos, freqs = i32([np.arange(5), np.arange(5) * 3]), torch.rand(16, dtype=torch.float64, device="cuda")
+    a = K.make_rope_cfg(2, 0, 64, 32, [0, 1] * 8, torch.float32)
+    b = K.RopeCfg(2, 0, 64, 32, 2, 0, 2, a.pair_axis)
+    outs = [torch.zeros_like(x) for _ in range(2)]
+    for cfg, out in zip((a, b), outs):
+        K.kvq_rope(cfg, x, None, pos, freqs, out, None)
+    assert torch.equal(*outs) and not torch.equal(outs[0], x)

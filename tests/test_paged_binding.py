@@ -35,3 +35,21 @@ def test_status_is_read_on_the_caches_device(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda d: type("S", (), {"cuda_stream": 1000 + d.index}))
     assert K.kvq_paged_get_status(c) == 128
     assert seen == [(3, 1003)] and current[0] == 0
+
+
+def test_rope_cfg_filled_by_hand():
+    """kvq_rope takes a RopeCfg that make_rope_cfg did not make: it says what is wrong with the
+    tensors (here: host memory), from the struct's own fields."""
+    axes = [0, 1] * 8
+    a = K.make_rope_cfg(2, 1, 64, 32, axes, torch.bfloat16)
+    b = K.RopeCfg(2, 1, 64, 32, 1, 0, 2, a.pair_axis)
+    q, k, pos, freqs = torch.zeros((3, 2, 64)).bfloat16(), torch.zeros((3, 1, 64)).bfloat16(), torch.zeros((2, 3), dtype=torch.int32), torch.zeros(16).double()
+    for cfg in (a, b):
+        with pytest.raises(ValueError, match="not on a CUDA device"):
+            K.kvq_rope(cfg, q, k, pos, freqs, q, k)
+        with pytest.raises(ValueError, match="positions"):
+            K.kvq_rope(cfg, q, k, pos[:1], freqs, q, k)
+        with pytest.raises(ValueError, match="q is"):
+            K.kvq_rope(cfg, q.half(), k, pos, freqs, q, k)
+    with pytest.raises(ValueError, match="float16, bfloat16 or float32"):
+        K.kvq_rope(K.RopeCfg(2, 1, 64, 32, 7, 0, 2, a.pair_axis), q, k, pos, freqs, q, k)
