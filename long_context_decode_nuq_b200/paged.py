@@ -54,8 +54,10 @@ class PagedSession:
         import torch
         self.slots = self._room("slots", max(tokens, 16), torch.int32)[:tokens]
         self.positions = self._room("positions", max(tokens, 16), torch.int32)[:tokens]
-        self.max_q, self.max_len = max_q, max_len or self.cfg.max_pages * self.cfg.page_tokens
-        need = K.kvq_paged_attention_workspace(self.cfg, self.requests, tokens, max_q, self.max_len)
+        self.max_q = max(max_q, 1)  # a step may be without tokens
+        self.max_len = max_len or self.cfg.max_pages * self.cfg.page_tokens
+        need = K.kvq_paged_attention_workspace(self.cfg, self.requests, tokens, self.max_q,
+                                               self.max_len)
         self.workspace = self._room("workspace", max(need, 16), torch.uint8)
         K.kvq_page_plan(self.caches[0], self.lens, n_new, self.table, self.free, self.n_free,
                         self.cu, self.lens, self.n_free, self.slots, self.positions)

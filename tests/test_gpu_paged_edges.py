@@ -5,6 +5,7 @@ import torch
 
 import long_context_decode_nuq_b200 as K
 import paged_testlib as R
+from long_context_decode_nuq_b200.paged import PagedSession
 
 pytestmark = pytest.mark.gpu
 DT = {"fp16": torch.float16, "bf16": torch.bfloat16}
@@ -115,6 +116,21 @@ def test_attention_sums_do_not_drift(B, Hkv, n, T, splits):
 
 
 # ------------------------------------------------------------------------------ together
+def test_session_steps_without_tokens():
+    cfg = K.make_paged_cfg(4, 2, 64, 16, 40, 20, torch.bfloat16)
+    rope = K.make_rope_cfg(4, 2, 64, 64, [0] * 32, torch.bfloat16)
+    freqs = 1e4 ** (-torch.arange(32, dtype=torch.float64, device="cuda") / 32)
+    s = PagedSession(cfg, 1, 2, rope, freqs)
+    for new in ([0, 0], [5, 0], [0, 0], [1, 1]):
+        n = sum(new)
+        q, k, v = (torch.randn((n, h, 64), device="cuda").bfloat16() for h in (4, 2, 2))
+        out = torch.full_like(q, float("nan"))
+        s.begin(i32(new), n, max(new))
+        s.attend(0, q, k, v, 0.125, out)
+        assert bool(torch.isfinite(out.float()).all())
+    assert s.lens.tolist() == [6, 1] and s.status() == 0
+
+
 def test_rope_cfg_filled_by_hand():
     x = torch.randn((5, 2, 64), device="cuda")
     pos, freqs = i32([np.arange(5), np.arange(5) * 3]), torch.rand(16, dtype=torch.float64, device="cuda")

@@ -53,3 +53,12 @@ def test_rope_cfg_filled_by_hand():
             K.kvq_rope(cfg, q.half(), k, pos, freqs, q, k)
     with pytest.raises(ValueError, match="float16, bfloat16 or float32"):
         K.kvq_rope(K.RopeCfg(2, 1, 64, 32, 7, 0, 2, a.pair_axis), q, k, pos, freqs, q, k)
+
+
+def test_session_begins_a_step_without_tokens():
+    """A step in which no request brings a token: refused only for its host memory, which comes last."""
+    from long_context_decode_nuq_b200.paged import PagedSession
+    s = PagedSession(K.make_paged_cfg(4, 2, 64, 16, 40, 20, torch.bfloat16), 1, 2, device="cpu")
+    with pytest.raises(ValueError, match="not on a CUDA device"):
+        s.begin(torch.zeros(2, dtype=torch.int32), 0, 0)
+    assert s.slots.numel() == s.positions.numel() == 0
