@@ -542,6 +542,14 @@ int kvq_page_plan(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_
                   int32_t* cu_new, int32_t* len_out, int32_t* n_free_out, int32_t* slots,
                   int32_t* positions, void* stream);
 
+/* kvq_page_plan for a list of free_entries entries: n_free, which lies on the device, counts as at
+ * most that (in kvq_page_plan as at most num_pages). */
+int kvq_page_plan_list(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_t B,
+                       const int32_t* len, const int32_t* n_new, int32_t* block_table,
+                       const int32_t* free_pages, int32_t free_entries, const int32_t* n_free,
+                       int32_t capacity, int32_t* cu_new, int32_t* len_out, int32_t* n_free_out,
+                       int32_t* slots, int32_t* positions, void* stream);
+
 /*
  * Give back the pages of finished requests: for each b with done[b] != 0, in request order, its
  * ceil(len[b]/P) pages go on top of the free list in table order, their table entries become -1

@@ -44,7 +44,7 @@ namespace {
 struct PlanArgs {
     const int32_t *len, *n_new, *free_pages, *n_free;
     int32_t *table, *cu, *len_out, *n_free_out, *slots, *pos, *status;
-    int32_t B, P, num_pages, max_pages, capacity;
+    int32_t B, P, num_pages, max_pages, capacity, entries;  // entries: of free_pages, at most num_pages
 };
 
 constexpr int kPlanThreads = 1024;
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
     const int lp = 31 - __clz(a.P), pm = a.P - 1;
     let_next();
     after_previous();
-    const int n_free = min(max(*a.n_free, 0), a.num_pages);
+    const int n_free = min(max(*a.n_free, 0), a.entries);
     long long tok0 = 0, page0 = 0;
     int bad = 0;
     if (tid == 0) s_used = 0;
@@ -512,20 +512,21 @@ int kvq_paged_get_status(const kvq_paged_cache* c, int32_t* out, void* stream) {
     return record_cuda(cudaStreamSynchronize(st));
 }
 
-int kvq_page_plan(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_t B,
-                  const int32_t* len, const int32_t* n_new, int32_t* block_table,
-                  const int32_t* free_pages, const int32_t* n_free, int32_t capacity,
-                  int32_t* cu_new, int32_t* len_out, int32_t* n_free_out, int32_t* slots,
-                  int32_t* positions, void* stream) {
+int kvq_page_plan_list(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_t B,
+                       const int32_t* len, const int32_t* n_new, int32_t* block_table,
+                       const int32_t* free_pages, int32_t free_entries, const int32_t* n_free,
+                       int32_t capacity, int32_t* cu_new, int32_t* len_out, int32_t* n_free_out,
+                       int32_t* slots, int32_t* positions, void* stream) {
     int e = check_paged_cfg(cfg);
     if (e) return e;
     if (!cache || !cache->status || !len || !n_new || !block_table || !free_pages || !n_free ||
         !cu_new || !len_out || !n_free_out)
         return KVQ_ERR_NULL;
     if (capacity > 0 && (!slots || !positions)) return KVQ_ERR_NULL;
-    if (B < 1 || B > (1 << 20) || capacity < 0 || capacity > (1 << 30)) return KVQ_ERR_SHAPE;
+    if (B < 1 || B > (1 << 20) || capacity < 0 || capacity > (1 << 30) || free_entries < 0) return KVQ_ERR_SHAPE;
+    const int32_t entries = free_entries < cfg->num_pages ? free_entries : cfg->num_pages;
     PlanArgs a{len,    n_new, free_pages, n_free, block_table,      cu_new,         len_out,        n_free_out, slots,
-               positions, cache->status, B, cfg->page_tokens, cfg->num_pages, cfg->max_pages, capacity};
+               positions, cache->status, B, cfg->page_tokens, cfg->num_pages, cfg->max_pages, capacity, entries};
     // a thread a request or token; one block up to 4096 tokens, since a cluster's start and its
     // barriers cost about a microsecond; four requests a thread where there are more than threads
     const int most = B > capacity ? B : capacity;
@@ -533,6 +534,15 @@ int kvq_page_plan(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_
     const int blocks = capacity > 4096 ? 8 : 1;
     cudaStream_t st = (cudaStream_t)stream;
     return B > threads ? launch_plan<4>(a, blocks, threads, st) : launch_plan<1>(a, blocks, threads, st);
+}
+
+int kvq_page_plan(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_t B,
+                  const int32_t* len, const int32_t* n_new, int32_t* block_table,
+                  const int32_t* free_pages, const int32_t* n_free, int32_t capacity,
+                  int32_t* cu_new, int32_t* len_out, int32_t* n_free_out, int32_t* slots,
+                  int32_t* positions, void* stream) {
+    return kvq_page_plan_list(cfg, cache, B, len, n_new, block_table, free_pages, INT32_MAX, n_free, capacity, cu_new,
+                              len_out, n_free_out, slots, positions, stream);
 }
 
 int kvq_page_release(const kvq_paged_cfg* cfg, const kvq_paged_cache* cache, int32_t B,

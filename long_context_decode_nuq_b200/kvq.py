@@ -36,8 +36,8 @@ EXPORTS = (
     "kvq_step_input_bytes", "kvq_step_workspace", "kvq_step_create", "kvq_step_launch",
     "kvq_step_destroy",
     "kvq_paged_validate_cfg", "kvq_paged_layout", "kvq_paged_reset", "kvq_paged_get_status",
-    "kvq_page_plan", "kvq_page_release", "kvq_paged_append", "kvq_paged_dequantize",
-    "kvq_paged_attention", "kvq_paged_attention_workspace", "kvq_rope",
+    "kvq_page_plan", "kvq_page_plan_list", "kvq_page_release", "kvq_paged_append",
+    "kvq_paged_dequantize", "kvq_paged_attention", "kvq_paged_attention_workspace", "kvq_rope",
 )
 
 
@@ -158,6 +158,8 @@ def load():
         "kvq_paged_reset": ([P, P], c_int),
         "kvq_paged_get_status": ([P, POINTER(c_int32), P], c_int),
         "kvq_page_plan": ([P, P, c_int32, P, P, P, P, P, c_int32, P, P, P, P, P, P], c_int),
+        "kvq_page_plan_list": ([P, P, c_int32, P, P, P, P, c_int32, P, c_int32, P, P, P, P, P, P],
+                               c_int),
         "kvq_page_release": ([P, P, c_int32, P, P, P, P, P, P], c_int),
         "kvq_paged_append": ([P, P, P, c_int64, P, c_int64, P, c_int32, P], c_int),
         "kvq_paged_dequantize": ([P, P, P, c_int32, P, P, P], c_int),
@@ -584,6 +586,7 @@ def _table(where, cache, table, B):
 
 def kvq_page_plan(cache: PagedCache, lens, n_new, block_table, free_pages, n_free, cu_new, len_out,
                   n_free_out, slots, positions, stream=None) -> None:
+    """n_free counts as at most the entries of free_pages (kvq_page_plan_list)."""
     w, B, cap = "kvq_page_plan", lens.numel(), slots.numel()
     _ints(w, cache.index, lens, n_new, free_pages, n_free, cu_new, len_out, n_free_out, slots,
           positions)
@@ -591,10 +594,10 @@ def kvq_page_plan(cache: PagedCache, lens, n_new, block_table, free_pages, n_fre
     if (n_new.numel() != B or cu_new.numel() != B + 1 or len_out.numel() != B
             or n_free.numel() != 1 or n_free_out.numel() != 1 or positions.numel() != cap):
         raise ValueError(f"{w}: sizes do not agree with {B} requests and {cap} tokens")
-    _call(w, load().kvq_page_plan, cache.index, stream, *cache.args, B, lens.data_ptr(),
-          n_new.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(), cap,
-          cu_new.data_ptr(), len_out.data_ptr(), n_free_out.data_ptr(), slots.data_ptr(),
-          positions.data_ptr())
+    _call(w, load().kvq_page_plan_list, cache.index, stream, *cache.args, B, lens.data_ptr(),
+          n_new.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), free_pages.numel(),
+          n_free.data_ptr(), cap, cu_new.data_ptr(), len_out.data_ptr(), n_free_out.data_ptr(),
+          slots.data_ptr(), positions.data_ptr())
 
 
 def kvq_page_release(cache: PagedCache, lens, done, block_table, free_pages, n_free,

@@ -87,6 +87,21 @@ def test_release_reports_entries_outside_the_pool():
     assert bool((table == -1).all()) and not lens.any()
 
 
+def test_plan_reads_no_further_than_its_list():
+    """A list of fewer entries than n_free says (here with more memory behind it, which names other
+    pages): what counts is the list."""
+    c = K.PagedCache(K.make_paged_cfg(1, 1, 64, 16, 20, 4, torch.bfloat16))
+    memory = i32([7, 8, 9, 0, 1, 2, 3, 4, 5, 6])
+    lens, new, table, n_free = i32([0, 0, 0]), i32([20, 33, 16]), i32(np.full((3, 4), -1)), i32([10])
+    slots, pos = i32([0] * 69), i32([0] * 69)
+    K.kvq_page_plan(c, lens, new, table, memory[:3], n_free, i32([0] * 4), lens, n_free, slots, pos)
+    # three pages: the first takes two, the second lacks three
+    assert table.tolist() == [[9, 8, -1, -1], [-1] * 4, [-1] * 4]
+    assert lens.tolist() == [20, 0, 0] and n_free.tolist() == [1]
+    assert slots.tolist() == list(range(144, 160)) + list(range(128, 132)) + [-1] * 49
+    assert K.kvq_paged_get_status(c) == K.KVQ_STATUS_NO_PAGES
+
+
 # ------------------------------------------------------------------------------ attention
 @pytest.mark.parametrize("B,Hkv,n,T,splits", [(1, 1, 1, 1 << 26, 1), (1, 1, 16, 1 << 26, 1), (5, 64, 1, 1 << 25, 0), (1, 1, 20, 1 << 26, 1), (1, 1, 1, 1 << 26, 0)])
 def test_attention_sums_do_not_drift(B, Hkv, n, T, splits):

@@ -62,3 +62,12 @@ def test_session_begins_a_step_without_tokens():
     with pytest.raises(ValueError, match="not on a CUDA device"):
         s.begin(torch.zeros(2, dtype=torch.int32), 0, 0)
     assert s.slots.numel() == s.positions.numel() == 0
+
+
+def test_plan_list_refuses_a_negative_size():
+    import ctypes
+    c = K.PagedCache(K.make_paged_cfg(1, 1, 64, 16, 10, 4, torch.bfloat16), device="cpu")
+    a = (ctypes.addressof((ctypes.c_uint8 * 512)()) + 255) & ~255
+    plan = K.load().kvq_page_plan_list
+    assert plan(*c.args, 3, a, a, a, a, -1, a, 7, a, a, a, a, a, None) == -3
+    assert plan(*c.args, 3, a, a, a, None, 5, a, 7, a, a, a, a, a, None) == -1
