@@ -471,9 +471,16 @@ def _dtype_code(dtype) -> int:
     return code
 
 
+def _int32(where, *sizes) -> None:
+    """ctypes cuts an int to 32 bits without a word."""
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+        raise ValueError(f"{where}: {sizes} do not fit 32 bits")
+
+
 def make_paged_cfg(Hq, Hkv, D, page_tokens, num_pages, max_pages, dtype, k_exp=0,
                    v_exp=0) -> PagedCfg:
     """dtype: torch.float16 or torch.bfloat16.  Raises KvqError where the library refuses it."""
+    _int32("make_paged_cfg", Hq, Hkv, D, page_tokens, num_pages, max_pages, k_exp, v_exp)
     cfg = PagedCfg(Hq, Hkv, D, page_tokens, num_pages, max_pages, _dtype_code(dtype), k_exp, v_exp)
     _check(load().kvq_paged_validate_cfg(byref(cfg)), "kvq_paged_validate_cfg")
     return cfg
@@ -634,6 +641,7 @@ def kvq_paged_dequantize(cache: PagedCache, slots, khat, vhat, stream=None) -> N
 
 def kvq_paged_attention_workspace(cfg: PagedCfg, B: int, total_q: int, max_q: int, max_len: int,
                                   splits: int = 0) -> int:
+    _int32("kvq_paged_attention_workspace", B, total_q, max_q, max_len, splits)
     n = c_size_t()
     _check(load().kvq_paged_attention_workspace(byref(cfg), B, total_q, max_q, max_len, splits,
                                                 byref(n)), "kvq_paged_attention_workspace")
@@ -646,6 +654,8 @@ def kvq_paged_attention(cache: PagedCache, q, cu_q, lens, block_table, max_q: in
     """cu_q: int32 [B + 1], or None for one query per request."""
     w, i, B, n = "kvq_paged_attention", cache.index, lens.numel(), q.shape[0]
     _ints(w, i, lens)
+    if (max_q | max_len | window | splits) >> 31:  # one of them negative or past 31 bits
+        _int32(w, max_q, max_len, window, splits)
     _table(w, cache, block_table, B)
     shape = n, *cache.q_row
     qs = _rows(w, "q", q, shape, cache.dtype, i)
@@ -680,6 +690,7 @@ def make_rope_cfg(Hq, Hkv, D, rot_dim, pair_axis, dtype, adjacent=False) -> Rope
     if len(axes) != rot_dim // 2 or len(axes) > 128 or min(axes, default=-1) < 0 or max(axes) > 7:
         raise ValueError(f"make_rope_cfg: pair_axis names an axis (0 .. 7) for each of the "
                          f"{rot_dim // 2} pairs")
+    _int32("make_rope_cfg", Hq, Hkv, D, rot_dim)
     cfg = RopeCfg(Hq, Hkv, D, rot_dim, _dtype_code(dtype), int(bool(adjacent)), max(axes) + 1,
                   (c_uint8 * 128)(*axes))
     cfg.py = _rope_shape(cfg)

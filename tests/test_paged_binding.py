@@ -71,3 +71,28 @@ def test_plan_list_refuses_a_negative_size():
     plan = K.load().kvq_page_plan_list
     assert plan(*c.args, 3, a, a, a, a, -1, a, 7, a, a, a, a, a, None) == -3
     assert plan(*c.args, 3, a, a, a, None, 5, a, 7, a, a, a, a, a, None) == -1
+
+
+@pytest.mark.parametrize("change", [dict(window=(1 << 32) + 5), dict(max_len=(1 << 32) + 64), dict(max_q=1 << 32 | 1), dict(splits=1 << 33),
+                                    dict(window=-(1 << 32))])
+def test_sizes_past_32_bits_are_refused(change):
+    """They would be cut to 32 bits on the way to the library: a window of 2^32 + 5 became 5."""
+    c = K.PagedCache(K.make_paged_cfg(8, 2, 128, 16, 10, 4, torch.bfloat16), device="cpu")
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    q = torch.zeros((3, 8, 128)).bfloat16()
+    kw = {**dict(max_q=1, max_len=64, window=0, splits=0), **change}
+    with pytest.raises(ValueError, match="32 bits"):
+        K.kvq_paged_attention(c, q, None, i(3), i(3, 4), sm_scale=0.1, out=q, **kw)
+    if "window" not in change:
+        kw.pop("window")
+        with pytest.raises(ValueError, match="32 bits"):
+            K.kvq_paged_attention_workspace(c.cfg, 3, 3, **kw)
+
+
+@pytest.mark.parametrize("change", [dict(num_pages=(1 << 32) + 10), dict(max_pages=1 << 32 | 4), dict(Hq=(1 << 32) + 8), dict(k_exp=1 << 32)])
+def test_configurations_past_32_bits_are_refused(change):
+    with pytest.raises(ValueError, match="32 bits"):
+        K.make_paged_cfg(**{**dict(Hq=8, Hkv=2, D=128, page_tokens=16, num_pages=10, max_pages=4, dtype=torch.bfloat16), **change})
+    if "Hq" in change:
+        with pytest.raises(ValueError, match="32 bits"):
+            K.make_rope_cfg(change["Hq"], 2, 128, 128, [0] * 64, torch.bfloat16)
