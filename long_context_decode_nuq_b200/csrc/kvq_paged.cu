@@ -276,8 +276,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 // store, to read back -- and walks over tokens with them, kAhead at a time so that their loads are
 // in flight together; a token's place in the pool costs a shift and a multiply, the rest of the
 // address is found once.  HBM bound, 2 + 9/16 bytes a value: 32768 tokens of 32 heads of 128 appended
-// in 118 us and read back in 115, 5.7 TB/s (87 % of the measured copy rate); with 8 channels to a
-// thread the two took 311 us instead of 247.
+// in 118 us and read back in 115, 5.8 TB/s (88 % of the measured copy rate); with 8 channels to a
+// thread the two calls took 311 us instead of 247.
 constexpr int kAppThreads = 256;
 constexpr int kAhead = 4;
 

@@ -19,8 +19,8 @@ namespace {
 //
 // Where the work is short (CL), a cluster of C blocks takes one (request, kv head) instead, an equal
 // part of its units each, and adds the parts through distributed shared memory: no search for the
-// block's place, no workspace and no second kernel (one request of
-// 1000 tokens, 8 kv heads: 8.8 us a call, 11.1 in a line with the join).
+// block's place, no workspace and no second kernel (one request of 1000 tokens, 8 kv heads: 9 us a
+// call, 11 in a line with the join).
 //
 // In a block one warp brings the codes: a stage is 32 tokens for each of the W others, a lane one
 // group of 16 tokens, which is one contiguous run of the pool.  The W warps take 32 tokens each,
@@ -40,10 +40,12 @@ namespace {
 // reads of V rows spread over the banks; S^T then leaves its lanes with (token, 2 rows), which
 // movmatrix turns into the B operand of the second product.
 //
-// Bound by issue, then HBM: 4 requests of up to 128 K tokens (3.1 M token-heads of 144 bytes, 32/8
-// heads) take 94-101 us a call with the join, 4.4-4.7 TB/s, at 18 warp instructions a token-head,
-// most of them conversions, scalings and matrix instructions; without either product the loads
-// alone take 78.  8 x 8 K with 32 kv heads: 55 us, about 10 of them start, end and join.
+// Bound by latencies that 16 warps an SM do not cover, none of its pipes being full: 4 requests of
+// up to 128 K tokens (3.1 M token-heads of 144 bytes, 32/8 heads) take 100 us a call with the join,
+// 4.4 TB/s (67 % of the measured copy rate), at 18 warp instructions a token-head, most of them
+// conversions, scalings and matrix instructions.  Issue slots are 60 % used, the tensor pipe 26 %;
+// warps wait for fixed latencies, the conversion pipe and memory in about equal parts.  8 x 8 K
+// with 32 kv heads: 55 us, about 10 of them start, end and join.
 constexpr int kUnit = 64;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(kFewThreads<NT>, 2) k_paged_attn(const AttnArg
                             if (!see) sc[gr][nt][z] = -INFINITY;
                         }
             }
-            // V is asked for here, to come while the softmax is computed (4 x 128K 97 -> 94 us)
+            // V is asked for here, to come while the softmax is computed (3 % at 4 x 128K)
             uint32_t vc[2][4][VW], sv[2][4];
 #pragma unroll
             for (int gr = 0; gr < 2; ++gr)
@@ -732,8 +734,9 @@ int64_t least_splits(int64_t span) { return (span + kSplitTokens - 1) / kSplitTo
 // block each, the others S, whose parts k_paged_merge adds.  The least time of a model in which a
 // block costs 10 us and 2 us per 128 tokens (measured: 2.0), blocks run one per SM in waves, and a
 // split writes and reads its part at 5 TB/s; whole units come in full waves, and there are none
-// where a split must not have all tokens.  Against 32768 tokens, 8 kv heads: 64 queries 514 us in
-// one part, 59 in 18; 1184 queries (152 units) 728 us all whole, 560 with the last 4 split.
+// where a split must not have all tokens.  Against 32768 tokens, 8 kv heads, in short runs: 64
+// queries 514 us in one part, 59 in 18; 1184 queries (152 units) 728 all whole, 560 with the last 4
+// split.
 void chunk_splits(const kvq_paged_cfg* c, int64_t units, int64_t span, int64_t* whole, int* splits) {
     const int64_t tiles = (span + 127) / 128, must = least_splits(span);
     const int64_t waves = must > 1 ? 0 : units / kSms, most = must > kSms ? must : kSms;

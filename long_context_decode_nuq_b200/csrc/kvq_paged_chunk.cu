@@ -26,10 +26,11 @@ namespace {
 //
 // Bound by the round trip between products and softmax: a step takes about 3700 cycles, 2048 of
 // them products; without the exponentials it would be 5 % less, without the conversions 11 %.
-// 2048 queries against 32768 tokens, 32/8 heads of 128: 933 us in short runs, 1022 in long ones at
-// the power limit, 1.14 and 1.04 PFLOP/s (69 and 63 % of a measured library product's rate).  Sixteen softmax warps of half a row each were slower (1187
-// against 1083 us), as were P in quarters (1061 against 1015) and part of the exponentials on the
-// multiply-add pipe (1034 against 1017).
+// 2048 queries against 32768 tokens, 32/8 heads of 128: 1017 us at the power limit, 1.05 PFLOP/s
+// (63 % of a measured library product's rate in a short run, 74 % of its sustained one); 933 in runs
+// too short to reach that limit.  Sixteen softmax warps of half a row each were slower (1187 against
+// 1083 us in runs of their time), as were P in quarters (1061 against 1015) and part of the
+// exponentials on the multiply-add pipe (1034 against 1017).
 constexpr int kRows = kChunkRows;   // 2 tiles of 128
 constexpr int kTok = 128;           // tokens a step
 constexpr int kSlots = 4;           // K or V tiles in shared memory

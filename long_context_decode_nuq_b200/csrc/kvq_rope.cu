@@ -11,7 +11,7 @@ namespace {
 // the remainder in binary32, once per (token, pair) into shared memory.  Then a thread keeps the 8
 // (cos, sin) of its 8 pairs in registers and turns them for one head after the other, two (four
 // for binary32) 16-byte loads and stores each.  HBM bound, each value read and written once: 32768
-// tokens of 40 heads of 128 in bf16 take 112-114 us, 5.9 TB/s (90 % of the measured copy rate).
+// tokens of 40 heads of 128 in bf16 take 115 us, 5.8 TB/s (89 % of the measured copy rate).
 constexpr int kRopeThreads = 256;
 
 struct RopeArgs {
